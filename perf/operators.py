@@ -287,7 +287,7 @@ def _plan(s):
     page, table = s["case"]["page"], s["block_table"]
     ctx, new = s["ctx_lens"].long(), s["new_lens"].long()
     have, need = (ctx + page - 1) // page, (ctx + new + page - 1) // page
-    more = need - have
+    more = torch.where(need <= table.shape[1], need - have, 0)
     last = more.cumsum(0)
     free = s["free_count"].long()
     ok = (need <= table.shape[1]) & ((more == 0) | (last <= free))
