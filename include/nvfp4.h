@@ -65,7 +65,7 @@
 extern "C" {
 #endif
 
-#define NVFP4_ABI_VERSION 8
+#define NVFP4_ABI_VERSION 9
 
 /* Size of a workspace (see the conventions above). */
 #define NVFP4_WORKSPACE_BYTES 66688
@@ -485,6 +485,245 @@ int nvfp4_quantize_rht(const nvfp4_quant_args* args, uint64_t sign_seed, hipStre
 int nvfp4_dequantize_rht(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
                          const float* amax, float global_fp8_max, int scale_fmt,
                          uint64_t sign_seed, float* out_f32, hipStream_t stream);
+
+/* ---------------------------------------------------------------------
+ * A paged NVFP4 key/value cache: planning a step's pages, normalising and
+ * rotating queries and keys, writing and reading the cache, attention over
+ * it.
+ *
+ * The cache of one layer holds num_pages pages of page_size tokens for
+ * kv_heads heads of head_dim values (D).  A slot is page * page_size + offset
+ * in the page, and a value is E2M1 code * E4M3 block scale * alpha with
+ * alpha = amax[head] / (6 * global_fp8_max): one calibrated outer amax per
+ * head, as the stale amaxes of nvfp4_quantize.  Blocks are 16 consecutive
+ * values of one token and head.  Keys lie token by token.  Values lie with
+ * the bytes of 8 consecutive tokens side by side, so that the attention's
+ * sum over tokens reads them as it multiplies them:
+ *   k_codes  [num_pages, kv_heads, page_size, D/2]
+ *   k_scales [num_pages, kv_heads, page_size, D/16]
+ *   v_codes  [num_pages, kv_heads, page_size/8, D/2, 8]
+ *   v_scales [num_pages, kv_heads, page_size/8, D/16, 8]
+ * page_size is a power of two from 8 to 1024; D is 64, 128, 192 or 256 (other
+ * multiples of 16: NVFP4_ERR_UNSUPPORTED); codes and scales are 16-byte
+ * aligned, amaxes 4-byte.  Bytes that no call has written may hold anything:
+ * no operator uses a token outside the lengths it is given.
+ */
+#define NVFP4_KV_MAX_HEADS 1024
+
+typedef struct nvfp4_kv_cache {
+  uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+  const float *k_amax, *v_amax; /* [kv_heads], device */
+  int64_t num_pages;            /* 1 .. 2^31 - 1 */
+  int kv_heads, page_size, head_dim;
+  float global_fp8_max;         /* S_g > 0: the value the cache is written with */
+} nvfp4_kv_cache;
+
+/*
+ * nvfp4_kv_plan -- the pages, slots and positions of a step's new tokens,
+ * from the requests' lengths, on the device.  Request b has ctx_lens[b]
+ * tokens in the cache, in the pages block_table[b, 0 .. ceil(ctx/page_size)),
+ * and brings new_lens[b] tokens (negative lengths count as 0); the step's
+ * tokens are the requests' new ones, request after request.
+ *   - A request whose ctx + new tokens need more than table_width pages is
+ *     refused.  The others take pages in order from the top of the stack
+ *     free_pages[0 .. *free_count): the i-th page taken is
+ *     free_pages[*free_count - 1 - i].  Once the running total of pages
+ *     needed passes *free_count, every request that needs a page is refused.
+ *     A refused request takes none; *refused counts them.
+ *   - block_table receives the new pages of the admitted requests; nothing
+ *     else of it changes.
+ *   - cu_new [batch + 1] = running total of new tokens; seq_lens [batch] =
+ *     ctx + new, or ctx where refused.
+ *   - positions [tokens]: the token's place in its request; slots [tokens]:
+ *     its slot, -1 for a refused request's token or where the table holds no
+ *     page of this cache.  Tokens from cu_new[batch] on (padding): 0 and -1.
+ *   - *free_count_out = *free_count - pages taken (the inputs stay, so the
+ *     call can be repeated).
+ * tokens >= the sum of new_lens, or the rest is not planned.  Pages are given
+ * back by writing their numbers to free_pages above the count.
+ * One launch.  Every pointer is a device pointer with natural alignment.
+ * Errors (NVFP4_ERR_INVALID): NULL pointers, batch, tokens or table_width
+ * < 0 or > 2^31 - 1, page_size not a power of two in 8 .. 1024, num_pages < 1
+ * or > 2^31 - 1.
+ */
+typedef struct nvfp4_kv_plan_args {
+  const int32_t *ctx_lens, *new_lens; /* [batch] */
+  int64_t batch;
+  int32_t* block_table;               /* [batch, table_width] */
+  int64_t table_width;
+  const int32_t* free_pages;          /* [num_pages] */
+  const int32_t* free_count;          /* [1], clamped to 0 .. num_pages */
+  int64_t num_pages;
+  int page_size;
+  int64_t tokens;
+  int32_t *cu_new, *seq_lens, *positions;
+  int64_t* slots;
+  int32_t *free_count_out, *refused;  /* [1] each */
+} nvfp4_kv_plan_args;
+
+int nvfp4_kv_plan(const nvfp4_kv_plan_args* args, hipStream_t stream);
+
+/*
+ * nvfp4_qk_norm_rope -- RMS norm of every query and key head and the position
+ * rotation, in one pass.  Per token t and head, x of D values:
+ *   n_i = x_i * (mean(x^2) + eps)^-1/2 * w_i           (w NULL: n = x)
+ *   (y_a, y_b) = (n_a c - n_b s, n_b c + n_a s)        per rotated pair
+ * with c, s = cos, sin[positions[t], j], j < rot_dim/2, and the pair j at
+ * (j, j + rot_dim/2) (NVFP4_PAIRS_HALVES) or (2j, 2j + 1)
+ * (NVFP4_PAIRS_NEIGHBOURS); values from rot_dim on are not rotated.  All of it
+ * in binary64, rounded once to binary32 and then to bf16: the bits then do
+ * not depend on the launch, and a key quantized behind it lands on the same
+ * side of every border as the formula's.  positions, cos and sin NULL with
+ * rot_dim = 0: no rotation.  A position outside [0, max_pos) gives NaN in the
+ * rotated values.
+ *   q, k       bf16 [tokens, heads, D], heads dense, q_stride / k_stride
+ *              elements from token to token (views of a fused projection);
+ *              multiples of 4, 8-byte aligned.  k may be NULL with k_heads = 0.
+ *   q_out, k_out  the same with strides of their own; may be q and k.
+ *   head_dim   a multiple of 32, at most 256; rot_dim a multiple of 32.
+ *   cos, sin   float [max_pos, rot_dim/2], 16-byte aligned.
+ *   q_weight, k_weight  bf16 [D], 8-byte aligned, or NULL.
+ * Errors (NVFP4_ERR_INVALID): NULL or misaligned pointers, tokens < 0, heads
+ * outside 0 .. NVFP4_KV_MAX_HEADS or both 0, head_dim not a positive multiple
+ * of 16, rot_dim not in 0 .. head_dim, strides < heads * D, eps negative or
+ * not finite, more than NVFP4_MAX_ELEMENTS elements; NVFP4_ERR_UNSUPPORTED:
+ * head_dim or rot_dim not a multiple of 32, or head_dim > 256.
+ */
+enum { NVFP4_PAIRS_HALVES = 0, NVFP4_PAIRS_NEIGHBOURS = 1 };
+
+typedef struct nvfp4_qk_args {
+  const uint16_t *q, *k;
+  int64_t tokens;
+  int q_heads, k_heads, head_dim;
+  int64_t q_stride, k_stride;
+  const int32_t* positions;           /* [tokens] */
+  const float *cos, *sin;
+  int64_t max_pos;
+  int rot_dim, pairs;
+  const uint16_t *q_weight, *k_weight;
+  float eps;
+  uint16_t *q_out, *k_out;
+  int64_t q_out_stride, k_out_stride;
+} nvfp4_qk_args;
+
+int nvfp4_qk_norm_rope(const nvfp4_qk_args* args, hipStream_t stream);
+
+/*
+ * nvfp4_qk_norm_rope_bwd -- its gradient.  With g = the incoming gradient
+ * rotated back, n = x * r and r = (mean(x^2) + eps)^-1/2:
+ *   dx = r * (g w - n * mean(g w n)),  dw = sum over tokens and heads of g n
+ * (w NULL: dx = g, no dw), in binary32, dw's sums in binary64 in a fixed
+ * order.  args->q, k and the tables as in the forward call; args->q_out and
+ * k_out with their strides are the OUTPUTS dq and dk (bf16); dq_out, dk_out
+ * the incoming gradients (bf16) with strides gq_stride and gk_stride.
+ *   dq_weight, dk_weight  float [D], required exactly where the weight is.
+ *   workspace   nvfp4_qk_norm_rope_bwd_workspace_bytes(head_dim) bytes of
+ *               device memory, 16-byte aligned, zero-filled once before its
+ *               first use (every completed call leaves its counter zero);
+ *               may be NULL without weights.  Calls that overlap need their
+ *               own.
+ * Errors: as the forward call, plus NULL or misaligned gradients, a weight
+ * without its gradient or the reverse, weights without workspace.
+ */
+size_t nvfp4_qk_norm_rope_bwd_workspace_bytes(int head_dim);
+int nvfp4_qk_norm_rope_bwd(const nvfp4_qk_args* args, const uint16_t* dq_out, int64_t gq_stride,
+                           const uint16_t* dk_out, int64_t gk_stride, float* dq_weight,
+                           float* dk_weight, void* workspace, hipStream_t stream);
+
+/*
+ * nvfp4_kv_append -- writes the keys and values of a step's tokens into the
+ * cache, normalising and rotating queries and keys on the way: qk as for
+ * nvfp4_qk_norm_rope (its k_out is not used: the key, rounded to bf16 as
+ * there, is quantized; q may be NULL with q_heads = 0), v [tokens, kv_heads,
+ * D] bf16 with v_stride.  Keys and values are quantized per 16 values as
+ * nvfp4_quantize does (E4M3 scales, round-to-nearest-even, the amax of the
+ * head as A and the cache's global_fp8_max as S_g) with args->select =
+ * NVFP4_SELECT_6 or NVFP4_SELECT_4OVER6.  Token t goes to slots[t]; a slot
+ * outside [0, num_pages * page_size) writes nothing (its query is still
+ * returned).  Slots of one call are distinct, or either token may be kept.
+ * Errors: as nvfp4_qk_norm_rope (qk.k, k_heads = cache.kv_heads and head_dim
+ * = cache.head_dim required) and the cache's rules; NULL or misaligned v or
+ * slots; another select -> NVFP4_ERR_INVALID (known rules:
+ * NVFP4_ERR_UNSUPPORTED).
+ */
+typedef struct nvfp4_kv_append_args {
+  nvfp4_qk_args qk;
+  const uint16_t* v;
+  int64_t v_stride;
+  const int64_t* slots;               /* [tokens] */
+  nvfp4_kv_cache cache;
+  int select;
+} nvfp4_kv_append_args;
+
+int nvfp4_kv_append(const nvfp4_kv_append_args* args, hipStream_t stream);
+
+/*
+ * nvfp4_kv_read -- the keys and values that `slots` hold, as bf16 [tokens,
+ * kv_heads, D] dense (the binary32 value of nvfp4_dequantize rounded to
+ * bf16).  A slot outside the cache reads as 0.  k_out or v_out may be NULL.
+ * Errors: the cache's rules, tokens < 0, slots NULL, misaligned (8-byte)
+ * outputs, both NULL (with tokens > 0) -> NVFP4_ERR_INVALID.
+ */
+int nvfp4_kv_read(const nvfp4_kv_cache* cache, const int64_t* slots, int64_t tokens,
+                  uint16_t* k_out, uint16_t* v_out, hipStream_t stream);
+
+/*
+ * nvfp4_kv_attention -- attention of a step's queries over the cache.
+ * Request b's queries are the rows cu_q[b] .. cu_q[b+1] of q (cu_q NULL: one
+ * query per request, tokens = batch) and are the last ones of its
+ * seq_lens[b] cached tokens: query i of n stands at position p = seq_len - n
+ * + i.  For query head h and its key/value head h / (q_heads / kv_heads):
+ *   s_j = scale * q . k_j over the attended j;  o = sum_j softmax(s)_j v_j
+ *   attended: 0 <= j < seq_len, j <= p if causal, j > p - window if window > 0
+ *   lse = log sum_j exp(s_j)
+ * A row that attends nothing gives o = 0 and lse = -inf; so do rows of q that
+ * belong to no request.  Tokens on a table entry that is no page of the cache
+ * (outside [0, num_pages)) are not attended, nor are tokens past table_width
+ * pages.  NaN and infinite values reach exactly the rows that attend them.
+ * Products of codes and block scales are exact in binary16; q is scaled by a
+ * power of two per row and held in binary16 (exact for values within 2^-14 of
+ * the row's largest, and nearer than 2^-25 of it below); scores, maxima, sums
+ * and outputs accumulate in binary32, the softmax weights round once to
+ * binary16 (relative 2^-11).
+ *   q         bf16 [tokens, q_heads, D], heads dense, q_stride from token to
+ *             token (a multiple of 8), 16-byte aligned.
+ *   out       bf16 [tokens, q_heads, D] dense, 16-byte aligned.
+ *   lse       optional float [tokens, q_heads].
+ *   max_seq_len  an upper bound of seq_lens that sizes the launch (longer
+ *             requests are still computed in full).
+ *   workspace nvfp4_kv_attention_workspace_bytes(args) bytes, 16-byte
+ *             aligned, whose first NVFP4_KV_ATTENTION_COUNTER_BYTES are zero
+ *             before its first use (every completed call leaves them zero);
+ *             may be NULL where that size is 0.  Overlapping calls need their
+ *             own.  The bytes depend on tokens, batch, max_seq_len, heads and
+ *             D alone.
+ * Errors (NVFP4_ERR_INVALID): the cache's rules, NULL or misaligned pointers,
+ * sizes < 0, q_heads not a positive multiple of kv_heads or above
+ * NVFP4_KV_MAX_HEADS, cu_q NULL with tokens != batch, scale not finite,
+ * window < 0, batch, tokens, table_width or max_seq_len > 2^31 - 1.
+ */
+#define NVFP4_KV_ATTENTION_COUNTER_BYTES 65536
+
+typedef struct nvfp4_kv_attention_args {
+  const uint16_t* q;
+  int64_t tokens, q_stride;
+  int q_heads;
+  nvfp4_kv_cache cache;
+  const int32_t* block_table;         /* [batch, table_width] */
+  int64_t batch, table_width;
+  const int32_t* seq_lens;            /* [batch] */
+  const int32_t* cu_q;                /* [batch + 1] or NULL */
+  int64_t max_seq_len;
+  float scale;
+  int causal;
+  int64_t window;                     /* 0: none */
+  uint16_t* out;
+  float* lse;
+  void* workspace;
+} nvfp4_kv_attention_args;
+
+size_t nvfp4_kv_attention_workspace_bytes(const nvfp4_kv_attention_args* args);
+int nvfp4_kv_attention(const nvfp4_kv_attention_args* args, hipStream_t stream);
 
 /* Static description of a status code. */
 const char* nvfp4_status_string(int status);

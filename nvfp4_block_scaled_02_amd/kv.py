@@ -1,0 +1,399 @@
+"""Torch-facing wrappers over the key/value-cache calls of libnvfp4.so
+(include/nvfp4.h): planning a step's pages, the norm and rotation of query and
+key heads, writing and reading the paged NVFP4 cache, attention over it.
+
+Argument marshalling only, as in api.py: every tensor is checked against the
+extent the kernels index, every call goes to the current stream of its
+device, and ``prepare(fn, ...)`` turns any of them into a ``Launch``.
+Projections (q, k, v, their gradients) may be views: their heads must be
+dense, their tokens may be any multiple of 4 values apart (8 for
+``kv_attention``).
+"""
+import ctypes
+from dataclasses import dataclass, field
+from typing import Optional
+
+import torch
+
+from . import _native as N
+from .api import _invoke, _need, _ptr, _SELECT, _stream, default_global_max
+
+_PAIRS = {"halves": N.PAIRS_HALVES, "neighbours": N.PAIRS_NEIGHBOURS}
+
+
+def _choice(table, value, name):
+    if value not in table:
+        raise ValueError(f"{name} must be one of {sorted(table)}, got {value!r}")
+    return table[value]
+
+
+def _heads(x: torch.Tensor, name, tokens=None, heads=None, dim=None, granule=4):
+    """[tokens, heads, D] bf16 on a GPU with dense heads: (tokens, heads, D,
+    elements from token to token)."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if x.device.type != "cuda":
+        raise ValueError(f"{name} must live on a GPU device, got {x.device}")
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {x.dtype}")
+    if x.dim() != 3:
+        raise ValueError(f"{name} must be 3-D [tokens, heads, head_dim]")
+    t, h, d = x.shape
+    if (tokens is not None and t != tokens) or (heads is not None and h != heads) or \
+            (dim is not None and d != dim):
+        raise ValueError(f"{name} must be [{tokens}, {heads if heads is not None else 'heads'}, "
+                         f"{dim if dim is not None else 'head_dim'}], got {tuple(x.shape)}")
+    st, sh, sd = x.stride()
+    if (d > 1 and sd != 1) or (h > 1 and sh != d):
+        raise ValueError(f"the heads of {name} must be dense (strides {x.stride()})")
+    if t <= 1:
+        st = h * d
+    elif st < h * d or st % granule:
+        raise ValueError(f"the tokens of {name} must be a multiple of {granule} values and at "
+                         f"least a token apart (strides {x.stride()})")
+    if x.data_ptr() % (2 * granule):
+        raise ValueError(f"{name} must be {2 * granule}-byte aligned")
+    return t, h, d, st
+
+
+# ---------------------------------------------------------------- cache
+@dataclass
+class KVCache:
+    """The paged NVFP4 cache of one layer: k_codes [P, H, S, D/2], k_scales
+    [P, H, S, D/16], v_codes [P, H, S/8, D/2, 8], v_scales [P, H, S/8, D/16, 8]
+    (uint8), the calibrated outer amaxes k_amax and v_amax [H] (float32) and
+    S_g.  Slot page * S + i is token i of a page."""
+    k_codes: torch.Tensor
+    k_scales: torch.Tensor
+    v_codes: torch.Tensor
+    v_scales: torch.Tensor
+    k_amax: torch.Tensor
+    v_amax: torch.Tensor
+    global_max: float
+    num_pages: int = field(init=False)
+    kv_heads: int = field(init=False)
+    page_size: int = field(init=False)
+    head_dim: int = field(init=False)
+
+    def __post_init__(self):
+        _need(self.k_codes, torch.uint8, "k_codes")
+        if self.k_codes.dim() != 4:
+            raise ValueError("k_codes must be [pages, heads, page_size, head_dim / 2]")
+        p, h, s, half = self.k_codes.shape
+        d = 2 * half
+        if d % 16:
+            raise ValueError(f"head_dim must be a multiple of 16, got {d}")
+        _need(self.k_scales, torch.uint8, "k_scales", p * h * s * (d // 16))
+        _need(self.v_codes, torch.uint8, "v_codes", p * h * s * half)
+        _need(self.v_scales, torch.uint8, "v_scales", p * h * s * (d // 16))
+        _need(self.k_amax, torch.float32, "k_amax", h)
+        _need(self.v_amax, torch.float32, "v_amax", h)
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim = p, h, s, d
+        self.global_max = float(self.global_max)
+        self._args = N.KVCacheArgs(
+            k_codes=_ptr(self.k_codes), k_scales=_ptr(self.k_scales), v_codes=_ptr(self.v_codes),
+            v_scales=_ptr(self.v_scales), k_amax=_ptr(self.k_amax), v_amax=_ptr(self.v_amax),
+            num_pages=p, kv_heads=h, page_size=s, head_dim=d, global_fp8_max=self.global_max)
+
+    @property
+    def device(self):
+        return self.k_codes.device
+
+
+def kv_cache(num_pages: int, kv_heads: int, page_size: int, head_dim: int, k_amax: torch.Tensor,
+             v_amax: torch.Tensor, *, global_max: float = 0.0, select: str = "4over6") -> KVCache:
+    """A new cache on the device of k_amax.  global_max 0: the default of the
+    selection rule it will be written with."""
+    dev = k_amax.device
+    z = lambda *n: torch.zeros(n, dtype=torch.uint8, device=dev)  # noqa: E731
+    return KVCache(z(num_pages, kv_heads, page_size, head_dim // 2),
+                   z(num_pages, kv_heads, page_size, head_dim // 16),
+                   z(num_pages, kv_heads, page_size // 8, head_dim // 2, 8),
+                   z(num_pages, kv_heads, page_size // 8, head_dim // 16, 8), k_amax, v_amax,
+                   float(global_max) or default_global_max("e4m3", select))
+
+
+# ---------------------------------------------------------------- plan
+@dataclass
+class KVPlan:
+    """What kv_plan returns: see nvfp4_kv_plan of include/nvfp4.h."""
+    cu_new: torch.Tensor
+    seq_lens: torch.Tensor
+    positions: torch.Tensor
+    slots: torch.Tensor
+    free_count: torch.Tensor
+    refused: torch.Tensor
+
+
+def kv_plan(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
+            free_pages: torch.Tensor, free_count: torch.Tensor, *, page_size: int, num_pages: int,
+            tokens: int, out: Optional[KVPlan] = None) -> KVPlan:
+    """The pages, slots and positions of a step's new tokens from the
+    requests' lengths; the new pages are written into block_table [batch,
+    width] (int32).  free_pages [num_pages] and free_count [1] (int32) are the
+    stack of free pages; the result's free_count is the count after the step.
+    tokens: at least the sum of new_lens (the rest is padding)."""
+    _need(ctx_lens, torch.int32, "ctx_lens")
+    batch = ctx_lens.numel()
+    _need(new_lens, torch.int32, "new_lens", batch)
+    _need(block_table, torch.int32, "block_table")
+    if block_table.dim() != 2 or block_table.shape[0] != batch:
+        raise ValueError(f"block_table must be [{batch}, width], got {tuple(block_table.shape)}")
+    _need(free_pages, torch.int32, "free_pages", num_pages)
+    _need(free_count, torch.int32, "free_count", 1)
+    dev = ctx_lens.device
+    if out is None:
+        e = lambda n, t=torch.int32: torch.empty(n, dtype=t, device=dev)  # noqa: E731
+        out = KVPlan(e(batch + 1), e(batch), e(tokens), e(tokens, torch.int64), e(1), e(1))
+    else:
+        _need(out.cu_new, torch.int32, "cu_new", batch + 1)
+        _need(out.seq_lens, torch.int32, "seq_lens", batch)
+        _need(out.positions, torch.int32, "positions", tokens)
+        _need(out.slots, torch.int64, "slots", tokens)
+        _need(out.free_count, torch.int32, "free_count", 1)
+        _need(out.refused, torch.int32, "refused", 1)
+    args = N.KVPlanArgs(
+        ctx_lens=_ptr(ctx_lens), new_lens=_ptr(new_lens), batch=batch,
+        block_table=_ptr(block_table), table_width=block_table.shape[1],
+        free_pages=_ptr(free_pages), free_count=_ptr(free_count), num_pages=num_pages,
+        page_size=page_size, tokens=tokens, cu_new=_ptr(out.cu_new), seq_lens=_ptr(out.seq_lens),
+        positions=_ptr(out.positions), slots=_ptr(out.slots), free_count_out=_ptr(out.free_count),
+        refused=_ptr(out.refused))
+    _invoke("nvfp4_kv_plan", (ctypes.byref(args),), dev,
+            (ctx_lens, new_lens, block_table, free_pages, free_count, out, args))
+    return out
+
+
+# ---------------------------------------------------------------- norm and rotation
+def rope_table(positions: int, rot_dim: int, *, base: float = 10000.0, device="cuda"):
+    """(cos, sin) float32 [positions, rot_dim / 2] of position * base^(-2j /
+    rot_dim), the angles in 64 bits."""
+    f = base ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+    a = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * f
+    return a.cos().float().contiguous(), a.sin().float().contiguous()
+
+
+def _qk(q, k, positions, cos, sin, q_weight, k_weight, eps, pairs):
+    """nvfp4_qk_args without outputs; q or k may be None."""
+    first = q if q is not None else k
+    if first is None:
+        raise ValueError("pass q, k or both")
+    a = N.QKArgs(eps=eps, pairs=_choice(_PAIRS, pairs, "pairs"))
+    t = d = None
+    for x, w, n in ((q, q_weight, "q"), (k, k_weight, "k")):
+        if x is None:
+            if w is not None:
+                raise ValueError(f"{n}_weight without {n}")
+            continue
+        t, h, d, st = _heads(x, n, t, None, d)
+        setattr(a, n, x.data_ptr())
+        setattr(a, n + "_heads", h)
+        setattr(a, n + "_stride", st)
+        if w is not None:
+            _need(w, torch.bfloat16, n + "_weight", d)
+            setattr(a, n + "_weight", w.data_ptr())
+    a.tokens, a.head_dim = t, d
+    if cos is None or sin is None or positions is None:
+        if not (cos is None and sin is None and positions is None):
+            raise ValueError("pass positions, cos and sin, or none of them")
+    else:
+        _need(cos, torch.float32, "cos")
+        if cos.dim() != 2 or cos.shape[1] * 2 > d:
+            raise ValueError(f"cos must be [positions, rot_dim / 2] with rot_dim <= {d}, "
+                             f"got {tuple(cos.shape)}")
+        _need(sin, torch.float32, "sin", cos.numel())
+        _need(positions, torch.int32, "positions", t)
+        a.positions, a.cos, a.sin = positions.data_ptr(), cos.data_ptr(), sin.data_ptr()
+        a.max_pos, a.rot_dim = cos.shape[0], 2 * cos.shape[1]
+    return a
+
+
+def _qk_out(a, x, given, n):
+    """Output of side n like x: given, or new and dense."""
+    if x is None:
+        return None
+    if given is None:
+        given = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+        st = x.shape[1] * x.shape[2]
+    else:
+        st = _heads(given, n + "_out", *x.shape)[3]
+    setattr(a, n + "_out", given.data_ptr())
+    setattr(a, n + "_out_stride", st)
+    return given
+
+
+def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor] = None,
+                 positions: Optional[torch.Tensor] = None, cos: Optional[torch.Tensor] = None,
+                 sin: Optional[torch.Tensor] = None, *, q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, pairs: str = "halves",
+                 out: Optional[tuple] = None):
+    """RMS norm of every head of q and k [tokens, heads, D] (where it has a
+    weight [D]) and rotation of its first 2 * cos.shape[1] values by the
+    angles of positions [tokens] (int32): (q_out, k_out).  out: (q_out,
+    k_out), which may be q and k."""
+    a = _qk(q, k, positions, cos, sin, q_weight, k_weight, eps, pairs)
+    qo, ko = out if out is not None else (None, None)
+    qo, ko = _qk_out(a, q, qo, "q"), _qk_out(a, k, ko, "k")
+    _invoke("nvfp4_qk_norm_rope", (ctypes.byref(a),), (q if q is not None else k).device,
+            (q, k, positions, cos, sin, q_weight, k_weight, qo, ko, a))
+    return qo, ko
+
+
+_BWD_WORKSPACES = {}
+
+
+def _capturing():
+    return torch.cuda.is_current_stream_capturing()
+
+
+def _cached_workspace(table, dev, nbytes, zeroed):
+    """A workspace of at least nbytes whose first `zeroed` bytes were zero
+    before its first use: one per (device, stream), made larger when needed.
+    Under graph capture a new one each call, as it belongs to the graph."""
+    if nbytes == 0:
+        return None
+    key = None if _capturing() else (dev.index, _stream(dev))
+    ws = table.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        ws[:zeroed].zero_()
+        if key is not None:
+            table[key] = ws
+    return ws
+
+
+def qk_norm_rope_bwd(dq_out: Optional[torch.Tensor], dk_out: Optional[torch.Tensor],
+                     q: Optional[torch.Tensor], k: Optional[torch.Tensor],
+                     positions: Optional[torch.Tensor] = None, cos: Optional[torch.Tensor] = None,
+                     sin: Optional[torch.Tensor] = None, *,
+                     q_weight: Optional[torch.Tensor] = None,
+                     k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                     pairs: str = "halves", out: Optional[dict] = None,
+                     workspace: Optional[torch.Tensor] = None):
+    """Gradient of qk_norm_rope at (q, k) for the gradients dq_out and dk_out
+    of its results: (dq, dk, dq_weight, dk_weight), the last two float32 [D]
+    or None.  out: optional {"dq", "dk", "dq_weight", "dk_weight"}."""
+    a = _qk(q, k, positions, cos, sin, q_weight, k_weight, eps, pairs)
+    out = dict(out or {})
+    dev = (q if q is not None else k).device
+    grads, strides, dws = [], [], []
+    for n, x, g, w in (("q", q, dq_out, q_weight), ("k", k, dk_out, k_weight)):
+        if (x is None) != (g is None):
+            raise ValueError(f"pass {n} and d{n}_out, or neither")
+        strides.append(_heads(g, f"d{n}_out", *x.shape)[3] if g is not None else 0)
+        grads.append(_qk_out(a, x, out.get("d" + n), n))
+        dw = None
+        if w is not None:
+            dw = out.get(f"d{n}_weight")
+            if dw is None:
+                dw = torch.empty(a.head_dim, dtype=torch.float32, device=dev)
+            _need(dw, torch.float32, f"d{n}_weight", a.head_dim)
+        dws.append(dw)
+    ws = None
+    if q_weight is not None or k_weight is not None:
+        n = N.lib().nvfp4_qk_norm_rope_bwd_workspace_bytes(a.head_dim)
+        if workspace is not None:
+            _need(workspace, torch.uint8, "workspace", n)
+            ws = workspace
+        else:
+            ws = _cached_workspace(_BWD_WORKSPACES, dev, n, 256)
+    _invoke("nvfp4_qk_norm_rope_bwd",
+            (ctypes.byref(a), _ptr(dq_out), strides[0], _ptr(dk_out), strides[1], _ptr(dws[0]),
+             _ptr(dws[1]), _ptr(ws)), dev,
+            (q, k, positions, cos, sin, q_weight, k_weight, dq_out, dk_out, grads, dws, ws, a))
+    return grads[0], grads[1], dws[0], dws[1]
+
+
+# ---------------------------------------------------------------- write and read
+def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, *,
+              q: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+              cos: Optional[torch.Tensor] = None, sin: Optional[torch.Tensor] = None,
+              q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+              eps: float = 1e-6, pairs: str = "halves", select: str = "4over6",
+              q_out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """Quantizes k (after its norm and rotation, as qk_norm_rope) and v
+    [tokens, kv_heads, D] into the cache at slots [tokens] (int64; a slot
+    outside the cache is skipped), and returns q after its norm and rotation
+    (None without q).  select: "6" or "4over6"."""
+    a = _qk(q, k, positions, cos, sin, q_weight, k_weight, eps, pairs)
+    t, st = a.tokens, _heads(v, "v", a.tokens, cache.kv_heads, cache.head_dim)[3]
+    _heads(k, "k", t, cache.kv_heads, cache.head_dim)
+    _need(slots, torch.int64, "slots", t)
+    qo = _qk_out(a, q, q_out, "q")
+    args = N.KVAppendArgs(qk=a, v=v.data_ptr(), v_stride=st, slots=slots.data_ptr(),
+                          cache=cache._args, select=_choice(_SELECT, select, "select"))
+    _invoke("nvfp4_kv_append", (ctypes.byref(args),), k.device,
+            (cache, q, k, v, slots, positions, cos, sin, q_weight, k_weight, qo, args))
+    return qo
+
+
+def kv_read(cache: KVCache, slots: torch.Tensor, *, out: Optional[tuple] = None):
+    """(k, v) bf16 [tokens, kv_heads, D]: what the cache holds at slots
+    (int64); 0 for a slot outside the cache."""
+    _need(slots, torch.int64, "slots")
+    n = slots.numel()
+    shape = (n, cache.kv_heads, cache.head_dim)
+    if out is None:
+        out = tuple(torch.empty(shape, dtype=torch.bfloat16, device=slots.device) for _ in "kv")
+    for o, name in zip(out, ("k_out", "v_out")):
+        _need(o, torch.bfloat16, name, n * shape[1] * shape[2])
+    _invoke("nvfp4_kv_read", (ctypes.byref(cache._args), _ptr(slots), n, _ptr(out[0]), _ptr(out[1])),
+            slots.device, (cache, slots, out))
+    return out
+
+
+# ---------------------------------------------------------------- attention
+_ATTENTION_WORKSPACES = {}
+
+
+def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
+                 seq_lens: torch.Tensor, cu_q: Optional[torch.Tensor] = None, *,
+                 max_seq_len: Optional[int] = None, scale: Optional[float] = None,
+                 causal: bool = True, window: int = 0, want_lse: bool = False,
+                 out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None):
+    """Attention of q [tokens, q_heads, D] over the cache: request b's queries
+    are rows cu_q[b] .. cu_q[b+1] (int32; None: one each) and the last of its
+    seq_lens[b] tokens (int32), whose pages block_table [batch, width] (int32)
+    names.  max_seq_len: an upper bound of seq_lens (default: the table's
+    width); scale: default D^-1/2; window: attend the last `window` tokens only
+    (0: all).  Returns out [tokens, q_heads, D] bf16, or (out, lse) with
+    want_lse.  workspace: a uint8 tensor of at least the size the library asks
+    for, zero-filled before its first use."""
+    t, h, d, st = _heads(q, "q", None, None, cache.head_dim, granule=8)
+    _need(seq_lens, torch.int32, "seq_lens")
+    batch = seq_lens.numel()
+    _need(block_table, torch.int32, "block_table")
+    if block_table.dim() != 2 or block_table.shape[0] != batch:
+        raise ValueError(f"block_table must be [{batch}, width], got {tuple(block_table.shape)}")
+    if cu_q is not None:
+        _need(cu_q, torch.int32, "cu_q", batch + 1)
+    elif t != batch:
+        raise ValueError(f"without cu_q every request has one query: {t} rows, {batch} requests")
+    dev = q.device
+    if out is None:
+        out = torch.empty((t, h, d), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(out, torch.bfloat16, "out", t * h * d)
+    if lse is None and want_lse:
+        lse = torch.empty((t, h), dtype=torch.float32, device=dev)
+    elif lse is not None:
+        _need(lse, torch.float32, "lse", t * h)
+    width = block_table.shape[1]
+    args = N.KVAttentionArgs(
+        q=q.data_ptr(), tokens=t, q_stride=st, q_heads=h, cache=cache._args,
+        block_table=_ptr(block_table), batch=batch, table_width=width, seq_lens=_ptr(seq_lens),
+        cu_q=_ptr(cu_q), max_seq_len=width * cache.page_size if max_seq_len is None else max_seq_len,
+        scale=d ** -0.5 if scale is None else scale, causal=int(causal), window=window,
+        out=_ptr(out), lse=_ptr(lse))
+    n = N.lib().nvfp4_kv_attention_workspace_bytes(ctypes.byref(args))
+    if workspace is not None:
+        _need(workspace, torch.uint8, "workspace")
+        if workspace.numel() < n:
+            raise ValueError(f"workspace must hold {n} bytes, got {workspace.numel()}")
+    else:
+        workspace = _cached_workspace(_ATTENTION_WORKSPACES, dev, n, N.KV_ATTENTION_COUNTER_BYTES)
+    args.workspace = _ptr(workspace)
+    _invoke("nvfp4_kv_attention", (ctypes.byref(args),), dev,
+            (q, cache, block_table, seq_lens, cu_q, out, lse, workspace, args))
+    return (out, lse) if lse is not None else out
