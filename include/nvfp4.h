@@ -669,8 +669,8 @@ int nvfp4_kv_read(const nvfp4_kv_cache* cache, const int64_t* slots, int64_t tok
 
 /*
  * nvfp4_kv_attention -- attention of a step's queries over the cache.
- * Request b's queries are the rows cu_q[b] .. cu_q[b+1] of q (cu_q NULL: one
- * query per request, tokens = batch) and are the last ones of its
+ * Request b's queries are the rows cu_q[b] .. cu_q[b+1] of q (cu_q[0] = 0,
+ * ascending; cu_q NULL: one query per request, tokens = batch) and are the last ones of its
  * seq_lens[b] cached tokens: query i of n stands at position p = seq_len - n
  * + i.  For query head h and its key/value head h / (q_heads / kv_heads):
  *   s_j = scale * q . k_j over the attended j;  o = sum_j softmax(s)_j v_j
@@ -700,7 +700,8 @@ int nvfp4_kv_read(const nvfp4_kv_cache* cache, const int64_t* slots, int64_t tok
  * Errors (NVFP4_ERR_INVALID): the cache's rules, NULL or misaligned pointers,
  * sizes < 0, q_heads not a positive multiple of kv_heads or above
  * NVFP4_KV_MAX_HEADS, cu_q NULL with tokens != batch, scale not finite,
- * window < 0, batch, tokens, table_width or max_seq_len > 2^31 - 1.
+ * window < 0, batch, tokens, table_width or max_seq_len > 2^31 - 1;
+ * NVFP4_ERR_UNSUPPORTED: table_width * page_size > 2^30.
  */
 #define NVFP4_KV_ATTENTION_COUNTER_BYTES 65536
 

@@ -166,6 +166,8 @@ static int attention_ok(const nvfp4_kv_attention_args& a) {
     return NVFP4_ERR_INVALID;
   if (!a.cu_q && a.tokens != a.batch) return NVFP4_ERR_INVALID;
   if (!isfinite(a.scale)) return NVFP4_ERR_INVALID;
+  // key positions, and their sums with a tile's width, stay in 32 bits
+  if (st == NVFP4_OK && a.table_width > ((int64_t)1 << 30) / a.cache.page_size) return NVFP4_ERR_UNSUPPORTED;
   return st;
 }
 
@@ -184,8 +186,8 @@ int nvfp4_kv_attention(const nvfp4_kv_attention_args* args, hipStream_t stream) 
   if (a.batch > 0 && (!given(a.seq_lens, 4) || (a.table_width > 0 && !given(a.block_table, 4))))
     return NVFP4_ERR_INVALID;
   if (st != NVFP4_OK) return st;
-  if (kv_attention_workspace(a) != 0 && !a.workspace) return NVFP4_ERR_INVALID;
   if (a.tokens == 0) return NVFP4_OK;
+  if (kv_attention_workspace(a) != 0 && !a.workspace) return NVFP4_ERR_INVALID;
   return status_of(launch_kv_attention(a, stream));
 }
 

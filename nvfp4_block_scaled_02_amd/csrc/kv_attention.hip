@@ -1,123 +1,709 @@
 // kv_attention.hip -- attention of a step's queries over the paged NVFP4
 // cache.
+//
+// The products run on the matrix units in binary16: E2M1 x E4M3 has 6
+// significant bits between 2^-10 and 2688, so a dequantized key or value
+// (without its outer scale) is a binary16 number exactly, and a query row is
+// scaled by a power of two to its largest value in [1, 2).  The outer scales,
+// the softmax scale, log2(e) and that power of two are one binary32 factor per
+// query row; the value's outer scale goes into the final division.
+//
+// A wavefront takes 16 * NQ query rows (token, head of one key/value head's
+// group) and walks tiles of 32 keys.  Per tile, with r = lane % 16, g = lane /
+// 16:
+//   S^T = K Q^T   two 16 x 16 products over D: lane (r, g) reads key 8 (r/4) +
+//     4 t + r % 4 and its values [g D/4, (g+1) D/4): whole 16-byte loads, and
+//     lane (n, g) receives the scores of query n with keys 8 g + 4 t + 0..3
+//   softmax       per lane, in the exponent of 2: the running maximum moves
+//     only when a score passes it by more than 2^8 (weights stay below 2^8,
+//     far inside binary16), so a tile usually needs no exchange between lanes
+//     and no rescaling; the sums stay per lane until the end
+//   O^T += V^T P^T  lane (m, g) reads keys 8 g .. 8 g + 7 of 4 value columns
+//     as the cache holds them (8 tokens side by side); lane (n, g)'s weights
+//     of keys 8 g .. 8 g + 7 are already the product's other operand.
+// No value passes through LDS and nothing is transposed.
+//
+// Few rows (decoding, drafted tokens): the four wavefronts of a workgroup
+// take every fourth tile and join through LDS, and long key ranges are split
+// over workgroups whose partial results (binary32) meet in the workspace; the
+// last workgroup to arrive joins them in order.  Many rows (prompts): each
+// wavefront has rows of its own and all walk the same keys.
 #include "kv.hpp"
 
 namespace nvfp4 {
 
-size_t kv_attention_workspace(const nvfp4_kv_attention_args&) { return 0; }
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
-// One wavefront per query row (token, head).  64 keys at a time: each lane
-// takes one key's dot product with the row in LDS, the running maximum and
-// sum of the softmax are kept per row, then each lane adds the weighted
-// values of its D / 64 value pairs.
+constexpr int kAttnThreads = 256;
+constexpr int kMaxSplits = 128;
+constexpr int kMaxGroups = NVFP4_KV_ATTENTION_COUNTER_BYTES / 4;
+constexpr int kSlabStride = 68;  // floats of a 64-column slab row: 4 apart in the banks
+constexpr float kLog2e = 1.44269504088896340736f;
+
+struct AttnPlan {
+  int nq;           // 16-row tiles of a wavefront
+  bool rows_split;  // wavefronts take rows of their own (else every fourth key tile)
+  int rows;         // rows of a workgroup
+  int splits;       // most workgroups over one tile's keys
+  int chunk;        // keys a workgroup is meant to take
+  int64_t tiles;    // row tiles over all requests, at most
+  int64_t grid;
+  size_t bytes;     // of workspace
+};
+
+struct AttnArgs {
+  nvfp4_kv_attention_args a;
+  int rows, splits, chunk, shift, group;
+  uint32_t tiles, tiles_per_request;
+};
+
+// ---------------------------------------------------------------- lanes
+__device__ __forceinline__ uint32_t u32(float v) { return __float_as_uint(v); }
+
+// max / sum over the four lanes of a query (lane % 16 equal), in all of them
+__device__ __forceinline__ float max_over_g(float v) {
+  auto a = __builtin_amdgcn_permlane32_swap(u32(v), u32(v), false, false);
+  v = __builtin_fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  auto b = __builtin_amdgcn_permlane16_swap(u32(v), u32(v), false, false);
+  return __builtin_fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float sum_over_g(float v) {
+  auto a = __builtin_amdgcn_permlane32_swap(u32(v), u32(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  auto b = __builtin_amdgcn_permlane16_swap(u32(v), u32(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+__device__ __forceinline__ f16x2 fp4_pair(uint32_t w, int sel) {
+  switch (sel) {
+    case 0: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0);
+    case 1: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1);
+    case 2: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2);
+    default: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3);
+  }
+}
+// two E4M3 bytes (the low or the high half of a word), 0x7F = NaN
+__device__ __forceinline__ f16x2 fp8_lo(uint32_t w) { return __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false); }
+__device__ __forceinline__ f16x2 fp8_hi(uint32_t w) { return __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true); }
+__device__ __forceinline__ f16x8 join8(f16x2 a, f16x2 b, f16x2 c, f16x2 d) {
+  return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// The tile as it lies in memory, for one lane.
 template <int D>
-__global__ void __launch_bounds__(64) kv_attention_kernel(nvfp4_kv_attention_args a) {
-  __shared__ float q[D];
-  __shared__ float p[64];
-  __shared__ int64_t at[64];  // page * kv_heads + head of the tile's keys, -1: not attended
-  const nvfp4_kv_cache& c = a.cache;
-  const int lane = threadIdx.x;
-  const int64_t token = blockIdx.x / a.q_heads;
-  const int h = (int)(blockIdx.x - token * a.q_heads), kvh = h / (a.q_heads / c.kv_heads);
-  // the request of this row
-  int64_t len = 0, pos = -1;
-  int64_t b = -1;
-  if (!a.cu_q) {
-    b = token;
-    len = a.seq_lens[b];
-    pos = len - 1;
-  } else {
-    for (int64_t i = 0; i < a.batch; ++i)
-      if (token >= a.cu_q[i] && token < a.cu_q[i + 1]) {
-        b = i;
-        len = a.seq_lens[b];
-        pos = len - (a.cu_q[i + 1] - token);
-        break;
-      }
+struct Raw {
+  static constexpr int NCH = D / 32;  // 8-value pieces of a key, and value pairs, per lane
+  uint32_t k[2][NCH];
+  uint32_t ks[2];    // block scales of the lane's pieces, one byte per two
+  uint4 v[NCH / 2];
+  uint2 vs[NCH / 2];
+  bool ok;           // the lane's 8 value tokens lie on a page of the cache
+};
+
+// Pages of the lane's key group and value group of a tile; -1: none.
+struct Pages {
+  int k, v;
+};
+
+// One tile's worth of addresses.  The table entry of a group past the last
+// key is that of the last one (its tokens are masked).
+struct Reader {
+  const nvfp4_kv_cache& c;
+  const int32_t* table;  // of the request
+  int last;              // last table entry that may be read
+  int shift, kvh, r, g;
+  __device__ __forceinline__ Pages pages(int tile0) const {
+    Pages p;
+    if (shift >= 5) {  // the tile lies in one page: a scalar load
+      const int i = tile0 >> shift;
+      p.k = p.v = table[i < last ? i : last];
+    } else {
+      const int ik = (tile0 + 8 * (r >> 2)) >> shift, iv = (tile0 + 8 * g) >> shift;
+      p.k = table[ik < last ? ik : last];
+      p.v = table[iv < last ? iv : last];
+    }
+    return p;
   }
-  const int shift = __builtin_ctz((unsigned)c.page_size);
-  const int64_t room = a.table_width << shift;
-  const int64_t hi0 = len < room ? len : room;
-  const int64_t hi = a.causal ? (hi0 < pos + 1 ? hi0 : pos + 1) : hi0;
-  int64_t lo = a.window > 0 ? pos - a.window + 1 : 0;
-  lo = lo < 0 ? 0 : lo;
-  for (int i = lane; i < D; i += 64)
-    q[i] = __uint_as_float((uint32_t)a.q[token * a.q_stride + (int64_t)h * D + i] << 16);
-  const float ks = outer_alpha(c.k_amax[kvh], c.global_fp8_max) * a.scale;
-  float m = -__builtin_inff(), l = 0.0f, o[D / 32] = {};
-  __syncthreads();
-  for (int64_t k0 = lo; k0 < hi; k0 += 64) {
-    const int64_t key = k0 + lane;
-    float s = -__builtin_inff();
-    int64_t ph = -1;
-    if (key < hi) {
-      const int64_t page = a.block_table[b * a.table_width + (key >> shift)];
-      if (page >= 0 && page < c.num_pages) {
-        ph = page * c.kv_heads + kvh;
-        const KvAddr k = {ph, (int)(key & (c.page_size - 1)), c.page_size, D};
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(c.k_codes + k.k_code());
-        const uint8_t* sc = c.k_scales + k.k_scale();
-        float dot = 0.0f;
-        for (int i = 0; i < D / 8; ++i) {
-          float v[8];
-          e2m1_unpack8(w[i], v);
-          float part = 0.0f;
-          for (int j = 0; j < 8; ++j) part = __builtin_fmaf(v[j], q[8 * i + j], part);
-          dot = __builtin_fmaf(part, decode_scale(FMT_E4M3, sc[i / 2]), dot);
+  template <int D>
+  __device__ __forceinline__ void load(int tile0, const Pages& p, Raw<D>& w) const {
+    constexpr int NCH = Raw<D>::NCH;
+    const uint32_t n = (uint32_t)c.num_pages;
+    const uint32_t pk = (uint32_t)p.k < n ? (uint32_t)p.k : 0u, pv = (uint32_t)p.v < n ? (uint32_t)p.v : 0u;
+    w.ok = (uint32_t)p.v < n;
+    const uint32_t ps = 1u << shift, mask = ps - 1;
+    // tokens from the start of the cache (page < 2^31, heads and page size <= 2^10)
+    const uint64_t head_tokens = (uint64_t)kvh << shift;
+    const uint64_t kt = (uint64_t)pk * (uint32_t)(c.kv_heads << shift) + head_tokens +
+                        (((uint32_t)tile0 + 8 * (r >> 2)) & mask) + (r & 3);
+    const uint64_t vt = (uint64_t)pv * (uint32_t)(c.kv_heads << shift) + head_tokens +
+                        (((uint32_t)tile0 + 8 * g) & mask);
+    const uint8_t* kc = c.k_codes + kt * (D / 2) + g * (D / 8);
+    const uint8_t* ks = c.k_scales + kt * (D / 16) + g * (NCH / 2);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const uint8_t* kct = kc + 4 * t * (D / 2);
+      if constexpr (NCH == 2) {
+        const uint2 x = *reinterpret_cast<const uint2*>(kct);
+        w.k[t][0] = x.x; w.k[t][1] = x.y;
+        w.ks[t] = ks[4 * t * (D / 16)];
+      } else if constexpr (NCH == 4) {
+        const uint4 x = *reinterpret_cast<const uint4*>(kct);
+        w.k[t][0] = x.x; w.k[t][1] = x.y; w.k[t][2] = x.z; w.k[t][3] = x.w;
+        w.ks[t] = *reinterpret_cast<const uint16_t*>(ks + 4 * t * (D / 16));
+      } else if constexpr (NCH == 6) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          const uint2 x = *reinterpret_cast<const uint2*>(kct + 8 * i);
+          w.k[t][2 * i] = x.x; w.k[t][2 * i + 1] = x.y;
         }
-        s = dot * ks;
+        const uint8_t* s = ks + 4 * t * (D / 16);
+        w.ks[t] = s[0] | (uint32_t)s[1] << 8 | (uint32_t)s[2] << 16;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint4 x = *reinterpret_cast<const uint4*>(kct + 16 * i);
+          w.k[t][4 * i] = x.x; w.k[t][4 * i + 1] = x.y; w.k[t][4 * i + 2] = x.z; w.k[t][4 * i + 3] = x.w;
+        }
+        w.ks[t] = *reinterpret_cast<const uint32_t*>(ks + 4 * t * (D / 16));
       }
     }
-    const bool any = ph >= 0;
-    float mt = s;
-    for (int d = 1; d < 64; d <<= 1) mt = __builtin_fmaxf(mt, __shfl_xor(mt, d));
-    const float mn = __builtin_fmaxf(m, mt);
-    const float base = mn == -__builtin_inff() ? 0.0f : mn;
-    const float e = any ? __expf(s - base) : 0.0f;
-    float lt = e;
-    for (int d = 1; d < 64; d <<= 1) lt += __shfl_xor(lt, d);
-    const float keep = m == -__builtin_inff() ? 0.0f : __expf(m - base);
-    l = l * keep + lt;
-    m = mn;
-    __syncthreads();
-    p[lane] = e;
-    at[lane] = ph;
-    __syncthreads();
-    for (int i = 0; i < D / 32; ++i) o[i] *= keep;
-    const int n = (int)(hi - k0 < 64 ? hi - k0 : 64);
-    for (int j = 0; j < n; ++j) {
-      if (at[j] < 0) continue;
-      const KvAddr k = {at[j], (int)((k0 + j) & (c.page_size - 1)), c.page_size, D};
-      for (int i = 0; i < (D + 127) / 128; ++i) {
-        const int e2 = 2 * (lane + 64 * i);  // first value of the pair
-        if (e2 >= D) break;
-        const f32x2 v = NVFP4_DEC_PK_FP4((uint32_t)c.v_codes[k.v_code() + 8 * (e2 / 2)], 0);
-        const float f = decode_scale(FMT_E4M3, c.v_scales[k.v_scale() + 8 * (e2 / 16)]);
-        o[2 * i] = __builtin_fmaf(p[j], v[0] * f, o[2 * i]);
-        o[2 * i + 1] = __builtin_fmaf(p[j], v[1] * f, o[2 * i + 1]);
+    const uint8_t* vc = c.v_codes + vt * (D / 2) + 16 * r;
+    const uint8_t* vs = c.v_scales + vt * (D / 16) + 8 * (r >> 2);
+#pragma unroll
+    for (int j = 0; j < NCH / 2; ++j) {
+      w.v[j] = *reinterpret_cast<const uint4*>(vc + 256 * j);
+      w.vs[j] = *reinterpret_cast<const uint2*>(vs + 32 * j);
+    }
+  }
+};
+
+// ---------------------------------------------------------------- one tile
+template <int D, int NQ>
+struct Walk {
+  static constexpr int NCH = D / 32, NJ = D / 64;
+  f16x8 q[NQ][NCH];
+  f32x4 o[NQ][NJ][4];  // [j][e][i]: query n, column 64 j + 16 g + 4 i + e
+  float factor[NQ];    // binary32 factor of a row's scores
+  float m[NQ], thr[NQ], base[NQ], l[NQ];
+  int lo[NQ], hi[NQ];  // keys that the row attends
+
+  // PARTIAL: some row does not attend some key of the tile.
+  template <bool PARTIAL>
+  __device__ __forceinline__ void tile(Raw<D>& w, int tile0, int g, int lo_any, int hi_any) {
+    f32x4 s[NQ][2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const f16x2 s01 = fp8_lo(w.ks[t]), s23 = fp8_hi(w.ks[t]);
+#pragma unroll
+      for (int c = 0; c < NCH; ++c) {
+        const _Float16 b = c / 2 == 0 ? s01[0] : c / 2 == 1 ? s01[1] : c / 2 == 2 ? s23[0] : s23[1];
+        const f16x2 f = {b, b};
+        const uint32_t x = w.k[t][c];
+        const f16x8 k = join8(fp4_pair(x, 0) * f, fp4_pair(x, 1) * f, fp4_pair(x, 2) * f, fp4_pair(x, 3) * f);
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+          s[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[n][c], c == 0 ? f32x4{0, 0, 0, 0} : s[n][t], 0, 0, 0);
+      }
+    }
+    const int key0 = tile0 + 8 * g;
+    f16x8 p[NQ], seen[NQ];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      float t[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        t[i] = s[n][i / 4][i % 4] * factor[n];
+        if constexpr (PARTIAL) {
+          const bool on = w.ok && key0 + i >= lo[n] && key0 + i < hi[n];
+          t[i] = on ? t[i] : -__builtin_inff();
+          seen[n][i] = on ? (_Float16)1.0f : (_Float16)0.0f;
+        }
+      }
+      float top = __builtin_fmaxf(__builtin_fmaxf(__builtin_fmaxf(t[0], t[1]), __builtin_fmaxf(t[2], t[3])),
+                                  __builtin_fmaxf(__builtin_fmaxf(t[4], t[5]), __builtin_fmaxf(t[6], t[7])));
+      if (__any(top > thr[n])) {
+        const float was = m[n];
+        m[n] = __builtin_fmaxf(m[n], max_over_g(top));
+        thr[n] = m[n] + 8.0f;
+        base[n] = m[n] == -__builtin_inff() ? 0.0f : m[n];
+        const float keep = was == m[n] || was == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(was - m[n]);
+        l[n] *= keep;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[n][j][e] *= keep;
+      }
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        t[i] = __builtin_amdgcn_exp2f(t[i] - base[n]);
+        sum += t[i];
+      }
+      l[n] += sum;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) p[n][i] = (_Float16)t[i];
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      uint2 vs = w.vs[j];
+      if constexpr (PARTIAL) {
+        // a token that no row attends may hold anything: its scales become 0
+        const int a = lo_any - key0, b = hi_any - key0;
+        uint64_t in = b <= 0 || !w.ok ? 0 : b >= 8 ? ~0ull : (1ull << (8 * b)) - 1;
+        in &= a <= 0 ? ~0ull : a >= 8 ? 0 : ~((1ull << (8 * a)) - 1);
+        vs.x &= (uint32_t)in;
+        vs.y &= (uint32_t)(in >> 32);
+        // a NaN scale on a token that some rows attend and others do not: 0 in
+        // the product, and NaN in the rows that attend it
+        f16x8 nan;
+        bool any = false;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const bool is = ((i < 4 ? vs.x : vs.y) >> (8 * (i % 4)) & 0x7Fu) == 0x7Fu;
+          nan[i] = is ? (_Float16)1.0f : (_Float16)0.0f;
+          any |= is;
+        }
+        if (__any(any)) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (nan[i] != (_Float16)0.0f) (i < 4 ? vs.x : vs.y) &= ~(0xFFu << (8 * (i % 4)));
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) {
+            const f32x4 hit = __builtin_amdgcn_mfma_f32_16x16x32_f16(nan, seen[n], f32x4{0, 0, 0, 0}, 0, 0, 0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[n][j][e][i] = hit[i] > 0.0f ? __builtin_nanf("") : o[n][j][e][i];
+          }
+        }
+      }
+      const f16x2 f0 = fp8_lo(vs.x), f1 = fp8_hi(vs.x), f2 = fp8_lo(vs.y), f3 = fp8_hi(vs.y);
+      // a byte holds two columns of one token; the products want two tokens of
+      // one column: nibbles of neighbouring bytes change places
+      const uint32_t M = 0x000F000Fu;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t x = h ? w.v[j].z : w.v[j].x, y = h ? w.v[j].w : w.v[j].y;
+        const uint32_t x4 = x >> 4, y4 = y >> 4, x8 = x >> 8, y8 = y >> 8;
+        const uint32_t xe = (x & M) | (x4 & ~M), ye = (y & M) | (y4 & ~M);
+        const uint32_t xo = (x4 & M) | (x8 & ~M), yo = (y4 & M) | (y8 & ~M);
+        const f16x8 ve = join8(fp4_pair(xe, 0) * f0, fp4_pair(xe, 2) * f1, fp4_pair(ye, 0) * f2, fp4_pair(ye, 2) * f3);
+        const f16x8 vo = join8(fp4_pair(xo, 0) * f0, fp4_pair(xo, 2) * f1, fp4_pair(yo, 0) * f2, fp4_pair(yo, 2) * f3);
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          o[n][j][2 * h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ve, p[n], o[n][j][2 * h], 0, 0, 0);
+          o[n][j][2 * h + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vo, p[n], o[n][j][2 * h + 1], 0, 0, 0);
+        }
+      }
+    }
+  }
+};
+
+// ---------------------------------------------------------------- workspace
+// Partial results of a split tile: per (tile, head) group and split, rows x
+// (D values, then maximum and sum), written and read where the whole GPU sees
+// them (no cache holds a stale copy).
+__device__ __forceinline__ void put2(float* p, float a, float b) {
+  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), (uint64_t)u32(b) << 32 | u32(a), __ATOMIC_RELAXED,
+                     __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float2 get2(const float* p) {
+  const uint64_t v = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED,
+                                       __HIP_MEMORY_SCOPE_AGENT);
+  return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+}
+
+// weight of a partial result with maximum m under the joint maximum M
+__device__ __forceinline__ float join_weight(float m, float M) {
+  return m == M ? 1.0f : __builtin_amdgcn_exp2f(m - M);
+}
+
+template <int D, int NQ, bool ROWS_SPLIT>
+__global__ void __launch_bounds__(kAttnThreads)
+kv_attention_kernel(AttnArgs args) {
+  constexpr int NCH = D / 32, NJ = D / 64, RW = 16 * NQ;
+  const nvfp4_kv_attention_args& a = args.a;
+  const nvfp4_kv_cache& c = a.cache;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+  // the workgroup's head, split and row tile; later tiles (whose causal key
+  // range is longer) first
+  const uint32_t kvh = blockIdx.x % (uint32_t)c.kv_heads;
+  uint32_t rest = blockIdx.x / (uint32_t)c.kv_heads;
+  const uint32_t split = rest % (uint32_t)args.splits;
+  rest /= (uint32_t)args.splits;
+  const uint32_t tile = args.tiles - 1 - rest;
+  // its request and rows
+  int64_t b, begin, end, local;
+  if (!a.cu_q) {
+    b = tile / args.tiles_per_request;
+    local = tile - (uint32_t)b * args.tiles_per_request;
+    begin = b;
+    end = b + 1;
+  } else {
+    // request b's tiles begin at floor(cu_q[b] * group / rows) + b; rows past
+    // cu_q[batch] count as a request of length 0.  64 probes at a time.
+    const auto cu = [&](int64_t i) {
+      const int64_t v = a.cu_q[i];
+      return v < 0 ? 0 : v < a.tokens ? v : a.tokens;
+    };
+    const auto start = [&](int64_t i) { return (uint64_t)cu(i) * (uint32_t)args.group / (uint32_t)args.rows + i; };
+    int64_t lo = 0, n = a.batch + 1;
+    while (n > 1) {
+      const int64_t step = (n + 63) / 64, i = lane * step;
+      const bool before = i < n && start(lo + i) <= tile;
+      const int hits = __popcll(__ballot(before));
+      const int64_t k = hits > 0 ? hits - 1 : 0;
+      lo += k * step;
+      n = n - k * step < step ? n - k * step : step;
+    }
+    b = lo;
+    local = (int64_t)tile - (int64_t)start(b);
+    if (local < 0) return;
+    begin = cu(b);
+    end = b < a.batch ? cu(b + 1) : a.tokens;
+    end = end < begin ? begin : end;
+  }
+  const int64_t rows = (end - begin) * args.group;  // of the request
+  const int64_t row0 = local * args.rows;           // of the workgroup
+  if (row0 >= rows) return;
+  const int count = (int)(rows - row0 < args.rows ? rows - row0 : args.rows);
+  // keys [0, len) of the request; its queries are the last ones
+  const int64_t seq = b < a.batch ? a.seq_lens[b] : 0;
+  const int64_t room = a.table_width << args.shift;
+  const int64_t len64 = seq < 0 ? 0 : seq < room ? seq : room;
+  const int len = (int)len64;
+  const int64_t pos0 = seq - (end - begin);  // position of the request's first query
+  const auto bounds = [&](int64_t row, int& lo, int& hi) {
+    const int64_t p = pos0 + row / args.group;
+    const int64_t h = a.causal && p + 1 < len ? p + 1 : len;
+    const int64_t w = a.window > 0 ? p - a.window + 1 : 0;
+    hi = (int)(h < 0 ? 0 : h);
+    lo = (int)(w < 0 ? 0 : w > len ? len : w);
+  };
+  // keys that any row attends, and those that all attend: bounds ascend with the row
+  const int first = ROWS_SPLIT ? wave * RW : 0;
+  int lo_any, hi_any, lo_all, hi_all;
+  {
+    const int last_row = ROWS_SPLIT ? (first + RW < count ? first + RW : count) - 1 : count - 1;
+    bounds(row0 + (ROWS_SPLIT ? (first < count ? first : 0) : 0), lo_any, hi_all);
+    bounds(row0 + (last_row > 0 ? last_row : 0), lo_all, hi_any);
+  }
+  if (ROWS_SPLIT && first >= count) return;  // no barrier follows in this form
+  // this workgroup's share
+  int k0 = lo_any & ~31, k1 = hi_any, nsplit = 1;
+  if constexpr (!ROWS_SPLIT) {
+    const int keys = k1 > k0 ? k1 - k0 : 0;
+    if (args.splits > 1) {
+      nsplit = (keys + args.chunk - 1) / args.chunk;
+      nsplit = nsplit < 1 ? 1 : nsplit < args.splits ? nsplit : args.splits;
+      const int each = ((keys + nsplit - 1) / nsplit + 127) & ~127;
+      nsplit = each > 0 ? (keys + each - 1) / each : 1;
+      nsplit = nsplit < 1 ? 1 : nsplit;
+      if ((int)split >= nsplit) return;
+      k0 += (int)split * each;
+      k1 = k1 - k0 < each ? k1 : k0 + each;
+    }
+  }
+
+  Walk<D, NQ> w;
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    int row = first + 16 * n + r;
+    row = row < count ? row : count - 1;  // the tile's spare rows repeat the last one
+    const int64_t rr = row0 + row, token = begin + rr / args.group;
+    bounds(rr, w.lo[n], w.hi[n]);
+    const uint16_t* src = a.q + token * a.q_stride +
+                          ((int64_t)kvh * args.group + rr % args.group) * D + g * (D / 4);
+    uint4 raw[NCH];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      raw[i] = *reinterpret_cast<const uint4*>(src + 8 * i);
+      const uint32_t t = chunk_abs_max_bits(raw[i]);
+      top = top > t ? top : t;
+    }
+    // the row's largest magnitude: bf16 patterns order like their values
+    float topf = __uint_as_float(top << 16);
+    topf = top >= 0x7F80u ? 1.0f : topf;  // infinities and NaN travel as they are
+    topf = max_over_g(topf);
+    int e = 254 - (int)(u32(topf) >> 23);  // exponent field of 2^-floor(log2 top)
+    e = topf == 0.0f ? 127 : e < 1 ? 1 : e > 254 ? 254 : e;
+    const float up = __uint_as_float((uint32_t)e << 23);
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        w.q[n][i][2 * k] = (_Float16)(bf16_lo(x[k]) * up);
+        w.q[n][i][2 * k + 1] = (_Float16)(bf16_hi(x[k]) * up);
+      }
+    }
+    w.factor[n] = __builtin_ldexpf(outer_alpha(c.k_amax[kvh], c.global_fp8_max) * a.scale * kLog2e, 127 - e);
+    w.m[n] = w.thr[n] = -__builtin_inff();
+    w.base[n] = w.l[n] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int e2 = 0; e2 < 4; ++e2) w.o[n][j][e2] = f32x4{0, 0, 0, 0};
+  }
+
+  // the walk: the next tile's bytes are in flight while one is computed, and
+  // the table entries of the one after
+  {
+    constexpr int STEP = ROWS_SPLIT ? 32 : 128;
+    const int t0 = k0 + (ROWS_SPLIT ? 0 : 32 * __builtin_amdgcn_readfirstlane(wave));
+    if (t0 < k1) {
+      const Reader rd = {c, a.block_table + b * a.table_width, (len - 1) >> args.shift, args.shift,
+                         (int)kvh, r, g};
+      Raw<D> cur, nxt;
+      Pages p = rd.pages(t0);
+      rd.load(t0, p, cur);
+      p = rd.pages(t0 + STEP < k1 ? t0 + STEP : t0);
+      for (int t = t0; t < k1; t += STEP) {
+        const int tn = t + STEP < k1 ? t + STEP : t;
+        rd.load(tn, p, nxt);
+        p = rd.pages(tn + STEP < k1 ? tn + STEP : tn);
+        const bool whole = t >= lo_all && t + 32 <= hi_all && __all(cur.ok);
+        if (whole) w.template tile<false>(cur, t, g, lo_any, hi_any);
+        else w.template tile<true>(cur, t, g, lo_any, hi_any);
+        cur = nxt;
+      }
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) w.l[n] = sum_over_g(w.l[n]);
+
+  const float av = outer_alpha(c.v_amax[kvh], c.global_fp8_max);
+  const auto out_row = [&](int row) {  // token * q_heads + head
+    const int64_t rr = row0 + row;
+    return (begin + rr / args.group) * a.q_heads + (int64_t)kvh * args.group + rr % args.group;
+  };
+
+  if constexpr (ROWS_SPLIT) {
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      const int row = first + 16 * n + r;
+      if (row >= count) continue;
+      const bool empty = w.m[n] == -__builtin_inff() && w.l[n] == 0.0f;
+      const float inv = empty ? 0.0f : av / w.l[n];
+      const int64_t at = out_row(row);
+      if (a.lse && g == 0) a.lse[at] = empty ? -__builtin_inff() : (w.m[n] + __builtin_log2f(w.l[n])) / kLog2e;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        uint32_t x[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[2 * i] = empty ? 0u : bf16_pair(w.o[n][j][0][i] * inv, w.o[n][j][1][i] * inv);
+          x[2 * i + 1] = empty ? 0u : bf16_pair(w.o[n][j][2][i] * inv, w.o[n][j][3][i] * inv);
+        }
+        uint4* dst = reinterpret_cast<uint4*>(a.out + at * D + 64 * j + 16 * g);
+        dst[0] = make_uint4(x[0], x[1], x[2], x[3]);
+        dst[1] = make_uint4(x[4], x[5], x[6], x[7]);
+      }
+    }
+  } else {
+    // join the four wavefronts: their maxima and sums, then 64 columns at a time
+    __shared__ __align__(16) float slab[4 * RW * kSlabStride];
+    __shared__ float ms[4][RW], ls[4][RW];
+    __shared__ bool last;
+    if (g == 0) {
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        ms[wave][16 * n + r] = w.m[n];
+        ls[wave][16 * n + r] = w.l[n];
       }
     }
     __syncthreads();
+    const size_t row_floats = D + 2;
+    const uint64_t group_at = (uint64_t)tile * (uint32_t)c.kv_heads + kvh;
+    float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + NVFP4_KV_ATTENTION_COUNTER_BYTES) +
+                   group_at * args.splits * RW * row_floats;
+    float* mine = parts + (size_t)split * RW * row_floats;
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      const int row = 16 * n + r;
+      const float M = __builtin_fmaxf(__builtin_fmaxf(ms[0][row], ms[1][row]), __builtin_fmaxf(ms[2][row], ms[3][row]));
+      const float f = join_weight(w.m[n], M);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w.o[n][j][e] *= f;
+    }
+    const int col = 4 * (threadIdx.x & 15);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      if (j) __syncthreads();
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        float* dst = slab + ((wave * RW) + 16 * n + r) * kSlabStride + 16 * g;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<float4*>(dst + 4 * i) =
+              make_float4(w.o[n][j][0][i], w.o[n][j][1][i], w.o[n][j][2][i], w.o[n][j][3][i]);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        const int row = 16 * n + (threadIdx.x >> 4);
+        if (row >= count) continue;
+        float M = ms[0][row];
+#pragma unroll
+        for (int v = 1; v < 4; ++v) M = __builtin_fmaxf(M, ms[v][row]);
+        float L = 0.0f;
+        float4 x = make_float4(0, 0, 0, 0);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          L += ls[v][row] * join_weight(ms[v][row], M);
+          const float4 y = *reinterpret_cast<const float4*>(slab + (v * RW + row) * kSlabStride + col);
+          x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+        }
+        if (nsplit == 1) {
+          const bool empty = M == -__builtin_inff() && L == 0.0f;
+          const float inv = empty ? 0.0f : av / L;
+          const int64_t at = out_row(row);
+          uint2 y = make_uint2(bf16_pair(x.x * inv, x.y * inv), bf16_pair(x.z * inv, x.w * inv));
+          if (empty) y = make_uint2(0, 0);
+          *reinterpret_cast<uint2*>(a.out + at * D + 64 * j + col) = y;
+          if (a.lse && j == 0 && col == 0) a.lse[at] = empty ? -__builtin_inff() : (M + __builtin_log2f(L)) / kLog2e;
+        } else {
+          float* dst = mine + (size_t)row * row_floats;
+          put2(dst + 64 * j + col, x.x, x.y);
+          put2(dst + 64 * j + col + 2, x.z, x.w);
+          if (j == 0 && col == 0) put2(dst + D, M, L);
+        }
+      }
+    }
+    if (nsplit == 1) return;
+    // arrive once the partial result has reached the level that all see
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    uint32_t* counter = static_cast<uint32_t*>(a.workspace) + group_at;
+    if (threadIdx.x == 0) {
+      last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)nsplit - 1;
+      if (last) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    if (!last) return;
+    // the last workgroup joins the splits in order: weights first (in the
+    // slab: at most 128 splits x 16 rows per pass), then the columns
+    float* wt = slab;  // [16 rows][kMaxSplits]
+#pragma unroll 1
+    for (int n = 0; n < NQ; ++n) {
+      const int row = 16 * n + (threadIdx.x >> 4), sub = threadIdx.x & 15;
+      const bool on = row < count;
+      const float* src = parts + (size_t)(on ? row : 0) * row_floats;
+      const size_t next = RW * row_floats;
+      float M = -__builtin_inff();
+      for (int s = sub; s < nsplit; s += 16) M = __builtin_fmaxf(M, get2(src + s * next + D).x);
+      M = __builtin_fmaxf(M, __uint_as_float(xor1_u32(u32(M))));
+      M = __builtin_fmaxf(M, __uint_as_float(xor2_u32(u32(M))));
+      M = __builtin_fmaxf(M, __uint_as_float(xor4_u32(u32(M))));
+      M = __builtin_fmaxf(M, __uint_as_float(xor8_u32(u32(M))));
+      float L = 0.0f;
+      __syncthreads();
+      for (int s = sub; s < nsplit; s += 16) {
+        const float2 ml = get2(src + s * next + D);
+        const float f = join_weight(ml.x, M);
+        wt[(threadIdx.x >> 4) * kMaxSplits + s] = f;
+        L += f * ml.y;
+      }
+      L += __uint_as_float(xor1_u32(u32(L)));
+      L += __uint_as_float(xor2_u32(u32(L)));
+      L += __uint_as_float(xor4_u32(u32(L)));
+      L += __uint_as_float(xor8_u32(u32(L)));
+      __syncthreads();
+      if (!on) continue;
+      const bool empty = M == -__builtin_inff() && L == 0.0f;
+      const float inv = empty ? 0.0f : av / L;
+      const int64_t at = out_row(row);
+      if (a.lse && sub == 0) a.lse[at] = empty ? -__builtin_inff() : (M + __builtin_log2f(L)) / kLog2e;
+      const float* f = wt + (threadIdx.x >> 4) * kMaxSplits;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        float4 x = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+        for (int s = 0; s < nsplit; ++s) {
+          const float2 y = get2(src + s * next + 64 * j + col), z = get2(src + s * next + 64 * j + col + 2);
+          x.x += f[s] * y.x; x.y += f[s] * y.y; x.z += f[s] * z.x; x.w += f[s] * z.y;
+        }
+        uint2 y = make_uint2(bf16_pair(x.x * inv, x.y * inv), bf16_pair(x.z * inv, x.w * inv));
+        if (empty) y = make_uint2(0, 0);
+        *reinterpret_cast<uint2*>(a.out + at * D + 64 * j + col) = y;
+      }
+    }
   }
-  const float va = outer_alpha(c.v_amax[kvh], c.global_fp8_max);
-  const bool empty = m == -__builtin_inff() && l == 0.0f;
-  const float inv = empty ? 0.0f : va / l;
-  uint16_t* out = a.out + (token * a.q_heads + h) * D;
-  for (int i = 0; i < (D + 127) / 128; ++i) {
-    const int e2 = 2 * (lane + 64 * i);
-    if (e2 >= D) break;
-    reinterpret_cast<uint32_t*>(out)[e2 / 2] = empty ? 0u : bf16_pair(o[2 * i] * inv, o[2 * i + 1] * inv);
+}
+
+// ---------------------------------------------------------------- host
+static AttnPlan plan_of(const nvfp4_kv_attention_args& a) {
+  AttnPlan p = {};
+  const int D = a.cache.head_dim, group = a.q_heads / a.cache.kv_heads;
+  // rows of an average request decide the form; every form is right for all
+  const int64_t batch = a.batch > 0 ? a.batch : 1;
+  const int64_t rows = a.cu_q ? (a.tokens * group + batch - 1) / batch : group;
+  const int nq_most = D <= 128 ? 4 : 2;  // registers: NQ * D accumulator values a lane / 16
+  p.nq = rows <= 16 ? 1 : rows <= 32 ? 2 : nq_most;
+  p.rows_split = rows >= 128;
+  p.rows = 16 * p.nq * (p.rows_split ? 4 : 1);
+  p.tiles = a.cu_q ? a.tokens * group / p.rows + a.batch + 1
+                   : a.batch * ((group + p.rows - 1) / p.rows);
+  const int64_t groups = p.tiles * a.cache.kv_heads;
+  int64_t keys = a.max_seq_len;
+  if (a.window > 0 && a.window + p.rows / group + 64 < keys) keys = a.window + p.rows / group + 64;
+  p.splits = 1;
+  p.chunk = 0x7FFFFF80;
+  if (!p.rows_split && groups <= kMaxGroups && keys > 128) {
+    // keys a workgroup takes: halved from 4096 until four workgroups for each
+    // compute unit have work at the bound, 128 (one tile a wavefront) at least
+    const int64_t want = 4 * (int64_t)device_cu_count();
+    int64_t chunk = 4096;
+    while (chunk > 128 && groups * ((keys + chunk - 1) / chunk) < want) chunk /= 2;
+    int64_t splits = (keys + chunk - 1) / chunk;
+    if (splits > kMaxSplits) splits = kMaxSplits;
+    p.splits = (int)splits;
+    p.chunk = (int)chunk;
   }
-  if (a.lse && lane == 0) a.lse[token * a.q_heads + h] = empty ? -__builtin_inff() : m + __logf(l);
+  p.grid = groups * p.splits;
+  p.bytes = p.splits > 1 ? NVFP4_KV_ATTENTION_COUNTER_BYTES +
+                               (size_t)groups * p.splits * 16 * p.nq * (D + 2) * sizeof(float)
+                         : 0;
+  return p;
+}
+
+size_t kv_attention_workspace(const nvfp4_kv_attention_args& a) { return plan_of(a).bytes; }
+
+template <int D, int NQ, bool ROWS_SPLIT>
+static void launch_one(const AttnArgs& x, int64_t grid, hipStream_t s) {
+  hipLaunchKernelGGL((kv_attention_kernel<D, NQ, ROWS_SPLIT>), dim3((unsigned)grid), dim3(kAttnThreads), 0, s, x);
+}
+
+template <int D>
+static void launch_dim(const AttnArgs& x, const AttnPlan& p, hipStream_t s) {
+  constexpr int MOST = D <= 128 ? 4 : 2;
+  if (p.rows_split) launch_one<D, MOST, true>(x, p.grid, s);
+  else if (p.nq == 1) launch_one<D, 1, false>(x, p.grid, s);
+  else if (p.nq == 2) launch_one<D, 2, false>(x, p.grid, s);
+  else launch_one<D, MOST, false>(x, p.grid, s);
 }
 
 hipError_t launch_kv_attention(const nvfp4_kv_attention_args& a, hipStream_t s) {
-  const dim3 grid((unsigned)(a.tokens * a.q_heads));
+  const AttnPlan p = plan_of(a);
+  if (p.grid > INT32_MAX) return hipErrorInvalidValue;
+  AttnArgs x = {};
+  x.a = a;
+  x.rows = p.rows;
+  x.splits = p.splits;
+  x.chunk = p.chunk;
+  x.shift = __builtin_ctz((unsigned)a.cache.page_size);
+  x.group = a.q_heads / a.cache.kv_heads;
+  x.tiles = (uint32_t)p.tiles;
+  x.tiles_per_request = (uint32_t)((x.group + p.rows - 1) / p.rows);
   switch (a.cache.head_dim) {
-    case 64: hipLaunchKernelGGL(kv_attention_kernel<64>, grid, dim3(64), 0, s, a); break;
-    case 128: hipLaunchKernelGGL(kv_attention_kernel<128>, grid, dim3(64), 0, s, a); break;
-    case 192: hipLaunchKernelGGL(kv_attention_kernel<192>, grid, dim3(64), 0, s, a); break;
-    default: hipLaunchKernelGGL(kv_attention_kernel<256>, grid, dim3(64), 0, s, a); break;
+    case 64: launch_dim<64>(x, p, s); break;
+    case 128: launch_dim<128>(x, p, s); break;
+    case 192: launch_dim<192>(x, p, s); break;
+    default: launch_dim<256>(x, p, s); break;
   }
   return hipGetLastError();
 }

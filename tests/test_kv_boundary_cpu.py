@@ -188,6 +188,10 @@ def test_attention_rejects(kw):
     assert _attn(**kw) == INV
 
 
+def test_attention_positions_stay_in_32_bits():
+    assert _attn(table_width=(1 << 26) + 1) == UNS
+
+
 def test_attention_empty_is_ok_and_workspace_is_required():
     assert _attn(tokens=0, q=None, out=None, workspace=None) == N.OK
     l = N.lib()
