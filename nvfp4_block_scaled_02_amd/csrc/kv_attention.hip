@@ -90,6 +90,12 @@ __device__ __forceinline__ f16x8 join8(f16x2 a, f16x2 b, f16x2 c, f16x2 d) {
   return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
+// largest of three, NaN if any is (v_maximum3_f32).  A builtin, not assembly:
+// the compiler has to see the read of a matrix result to wait for it.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c);
+}
+
 // The tile as it lies in memory, for one lane.
 template <int D>
 struct Raw {
@@ -185,12 +191,11 @@ struct Walk {
   f16x8 q[NQ][NCH];
   f32x4 o[NQ][NJ][4];  // [j][e][i]: query n, column 64 j + 16 g + 4 i + e
   float factor[NQ];    // binary32 factor of a row's scores
-  float m[NQ], thr[NQ], base[NQ], l[NQ];
+  float m[NQ], thr[NQ], l[NQ];
   int lo[NQ], hi[NQ];  // keys that the row attends
 
-  // PARTIAL: some row does not attend some key of the tile.
-  template <bool PARTIAL>
-  __device__ __forceinline__ void tile(Raw<D>& w, int tile0, int g, int lo_any, int hi_any) {
+  // partial: some row does not attend some key of the tile.
+  __device__ __forceinline__ void tile(Raw<D>& w, int tile0, int g, int lo_any, int hi_any, bool partial) {
     f32x4 s[NQ][2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -207,26 +212,25 @@ struct Walk {
       }
     }
     const int key0 = tile0 + 8 * g;
-    f16x8 p[NQ], seen[NQ];
+    if (partial) {
+#pragma unroll
+      for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (!attends(n, key0 + i, w.ok)) s[n][i / 4][i % 4] = -__builtin_inff();
+      hide_values(w, key0, lo_any, hi_any);
+    }
+    f16x8 p[NQ];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
-      float t[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        t[i] = s[n][i / 4][i % 4] * factor[n];
-        if constexpr (PARTIAL) {
-          const bool on = w.ok && key0 + i >= lo[n] && key0 + i < hi[n];
-          t[i] = on ? t[i] : -__builtin_inff();
-          seen[n][i] = on ? (_Float16)1.0f : (_Float16)0.0f;
-        }
-      }
-      float top = __builtin_fmaxf(__builtin_fmaxf(__builtin_fmaxf(t[0], t[1]), __builtin_fmaxf(t[2], t[3])),
-                                  __builtin_fmaxf(__builtin_fmaxf(t[4], t[5]), __builtin_fmaxf(t[6], t[7])));
+      const f32x4 s0 = s[n][0], s1 = s[n][1];
+      // factor >= 0: the largest product is that of the largest score.  A NaN
+      // score never moves the maximum; its weight and the row become NaN.
+      const float top = factor[n] * max3(max3(s0[0], s0[1], s0[2]), max3(s0[3], s1[0], s1[1]), max3(s1[2], s1[3], s1[3]));
       if (__any(top > thr[n])) {
         const float was = m[n];
         m[n] = __builtin_fmaxf(m[n], max_over_g(top));
         thr[n] = m[n] + 8.0f;
-        base[n] = m[n] == -__builtin_inff() ? 0.0f : m[n];
         const float keep = was == m[n] || was == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(was - m[n]);
         l[n] *= keep;
 #pragma unroll
@@ -234,10 +238,11 @@ struct Walk {
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[n][j][e] *= keep;
       }
-      float sum = 0.0f;
+      const float base = m[n] == -__builtin_inff() ? 0.0f : -m[n];
+      float t[8], sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        t[i] = __builtin_amdgcn_exp2f(t[i] - base[n]);
+        t[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(i < 4 ? s0[i % 4] : s1[i % 4], factor[n], base));
         sum += t[i];
       }
       l[n] += sum;
@@ -246,38 +251,7 @@ struct Walk {
     }
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      uint2 vs = w.vs[j];
-      if constexpr (PARTIAL) {
-        // a token that no row attends may hold anything: its scales become 0
-        const int a = lo_any - key0, b = hi_any - key0;
-        uint64_t in = b <= 0 || !w.ok ? 0 : b >= 8 ? ~0ull : (1ull << (8 * b)) - 1;
-        in &= a <= 0 ? ~0ull : a >= 8 ? 0 : ~((1ull << (8 * a)) - 1);
-        vs.x &= (uint32_t)in;
-        vs.y &= (uint32_t)(in >> 32);
-        // a NaN scale on a token that some rows attend and others do not: 0 in
-        // the product, and NaN in the rows that attend it
-        f16x8 nan;
-        bool any = false;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const bool is = ((i < 4 ? vs.x : vs.y) >> (8 * (i % 4)) & 0x7Fu) == 0x7Fu;
-          nan[i] = is ? (_Float16)1.0f : (_Float16)0.0f;
-          any |= is;
-        }
-        if (__any(any)) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (nan[i] != (_Float16)0.0f) (i < 4 ? vs.x : vs.y) &= ~(0xFFu << (8 * (i % 4)));
-#pragma unroll
-          for (int n = 0; n < NQ; ++n) {
-            const f32x4 hit = __builtin_amdgcn_mfma_f32_16x16x32_f16(nan, seen[n], f32x4{0, 0, 0, 0}, 0, 0, 0);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) o[n][j][e][i] = hit[i] > 0.0f ? __builtin_nanf("") : o[n][j][e][i];
-          }
-        }
-      }
+      const uint2 vs = w.vs[j];
       const f16x2 f0 = fp8_lo(vs.x), f1 = fp8_hi(vs.x), f2 = fp8_lo(vs.y), f3 = fp8_hi(vs.y);
       // a byte holds two columns of one token; the products want two tokens of
       // one column: nibbles of neighbouring bytes change places
@@ -296,6 +270,46 @@ struct Walk {
           o[n][j][2 * h + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vo, p[n], o[n][j][2 * h + 1], 0, 0, 0);
         }
       }
+    }
+  }
+
+  __device__ __forceinline__ bool attends(int n, int key, bool ok) const {
+    return ok && key >= lo[n] && key < hi[n];
+  }
+
+  // In a tile that some rows attend in part: the scales of values that no row
+  // attends (which may be anything) become 0; a NaN scale becomes 0 too, and
+  // the rows that attend it get their NaN here.
+  __device__ __forceinline__ void hide_values(Raw<D>& w, int key0, int lo_any, int hi_any) {
+    const int a = lo_any - key0, b = hi_any - key0;
+    uint64_t in = b <= 0 || !w.ok ? 0 : b >= 8 ? ~0ull : (1ull << (8 * b)) - 1;
+    in &= a <= 0 ? ~0ull : a >= 8 ? 0 : ~((1ull << (8 * a)) - 1);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      uint32_t s[2] = {w.vs[j].x & (uint32_t)in, w.vs[j].y & (uint32_t)(in >> 32)};
+      // bytes equal to 0x7F: bit 7 of (byte & 0x7F) + 1
+      const uint32_t nan0 = ((s[0] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+      const uint32_t nan1 = ((s[1] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+      if (__any((nan0 | nan1) != 0)) {
+        f16x8 nan;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          nan[i] = ((i < 4 ? nan0 : nan1) >> (8 * (i % 4)) & 0x80u) ? (_Float16)1.0f : (_Float16)0.0f;
+        s[0] &= ~((nan0 >> 7) * 0xFFu);
+        s[1] &= ~((nan1 >> 7) * 0xFFu);
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          f16x8 seen;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) seen[i] = attends(n, key0 + i, w.ok) ? (_Float16)1.0f : (_Float16)0.0f;
+          const f32x4 hit = __builtin_amdgcn_mfma_f32_16x16x32_f16(nan, seen, f32x4{0, 0, 0, 0}, 0, 0, 0);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[n][j][e][i] = hit[i] > 0.0f ? __builtin_nanf("") : o[n][j][e][i];
+        }
+      }
+      w.vs[j] = make_uint2(s[0], s[1]);
     }
   }
 };
@@ -319,8 +333,14 @@ __device__ __forceinline__ float join_weight(float m, float M) {
   return m == M ? 1.0f : __builtin_amdgcn_exp2f(m - M);
 }
 
+// Wavefronts of a SIMD that the registers are shared out for: as many as fit
+// without spilling (512 registers a lane at one wavefront).
+constexpr int attn_waves(int D, int NQ) {
+  return D * NQ <= 64 ? 4 : D * NQ <= 128 ? 3 : D * NQ <= 256 ? 2 : 1;
+}
+
 template <int D, int NQ, bool ROWS_SPLIT>
-__global__ void __launch_bounds__(kAttnThreads)
+__global__ void __launch_bounds__(kAttnThreads, attn_waves(D, NQ))
 kv_attention_kernel(AttnArgs args) {
   constexpr int NCH = D / 32, NJ = D / 64, RW = 16 * NQ;
   const nvfp4_kv_attention_args& a = args.a;
@@ -429,7 +449,8 @@ kv_attention_kernel(AttnArgs args) {
     topf = max_over_g(topf);
     int e = 254 - (int)(u32(topf) >> 23);  // exponent field of 2^-floor(log2 top)
     e = topf == 0.0f ? 127 : e < 1 ? 1 : e > 254 ? 254 : e;
-    const float up = __uint_as_float((uint32_t)e << 23);
+    // a negative scale turns the row's sign, so that factor >= 0
+    const float up = __builtin_copysignf(__uint_as_float((uint32_t)e << 23), a.scale);
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
       const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
@@ -439,9 +460,11 @@ kv_attention_kernel(AttnArgs args) {
         w.q[n][i][2 * k + 1] = (_Float16)(bf16_hi(x[k]) * up);
       }
     }
-    w.factor[n] = __builtin_ldexpf(outer_alpha(c.k_amax[kvh], c.global_fp8_max) * a.scale * kLog2e, 127 - e);
+    w.factor[n] = __builtin_ldexpf(outer_alpha(c.k_amax[kvh], c.global_fp8_max) * __builtin_fabsf(a.scale) * kLog2e, 127 - e);
+    // a score of -inf stays below every other one
+    w.factor[n] = w.factor[n] == 0.0f ? 0x1p-126f : w.factor[n];
     w.m[n] = w.thr[n] = -__builtin_inff();
-    w.base[n] = w.l[n] = 0.0f;
+    w.l[n] = 0.0f;
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
@@ -465,8 +488,7 @@ kv_attention_kernel(AttnArgs args) {
         rd.load(tn, p, nxt);
         p = rd.pages(tn + STEP < k1 ? tn + STEP : tn);
         const bool whole = t >= lo_all && t + 32 <= hi_all && __all(cur.ok);
-        if (whole) w.template tile<false>(cur, t, g, lo_any, hi_any);
-        else w.template tile<true>(cur, t, g, lo_any, hi_any);
+        w.tile(cur, t, g, lo_any, hi_any, !whole);
         cur = nxt;
       }
     }
