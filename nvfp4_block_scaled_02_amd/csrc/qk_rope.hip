@@ -5,42 +5,49 @@
 
 namespace nvfp4 {
 
-// One wavefront per 64 / LPH heads of a token: a lane reads 16 bytes and
-// writes 16.
+// A lane reads 16 bytes of a head and writes 16; the next group's bytes are in
+// flight while one is computed.
 template <int LPH, int PAIRS>
 __global__ void __launch_bounds__(kRowThreads)
-qk_norm_rope_kernel(nvfp4_qk_args a, int64_t tasks, int per_token) {
-  const RowMap<LPH> m(a.head_dim, a.rot_dim, PAIRS);
-  const int heads = a.q_heads + a.k_heads;
-  const double inv_d = 1.0 / a.head_dim;
-  for (int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); w < tasks; w += (int64_t)gridDim.x * 4) {
-    const RowTask t = row_task<LPH>(w, per_token);
-    const bool on = t.head < heads;
-    const bool isq = t.head < a.q_heads;
-    const int h = isq ? t.head : t.head - a.q_heads;
-    RowMap<LPH> mm = m;
-    mm.active = m.active && on;
-    const RowAngles g = row_angles(a, mm, t.token);
-    float x[8];
-    row_load(isq ? a.q + t.token * a.q_stride + (int64_t)h * a.head_dim
-                 : a.k + t.token * a.k_stride + (int64_t)h * a.head_dim, mm, x);
-    uint2 o0, o1;
-    row_norm_rope<LPH, PAIRS>(x, mm, isq ? a.q_weight : a.k_weight, a.eps, inv_d, g, o0, o1);
-    row_store(isq ? a.q_out + t.token * a.q_out_stride + (int64_t)h * a.head_dim
-                  : a.k_out + t.token * a.k_out_stride + (int64_t)h * a.head_dim, mm, o0, o1);
+qk_norm_rope_kernel(nvfp4_qk_args a, RowGrid grid) {
+  constexpr int N = 64 / LPH;
+  const int D = a.head_dim, sub = (int)(threadIdx.x & 63) / LPH;
+  const RowMap<LPH> m(D, a.rot_dim, PAIRS);
+  const Row8 wq = weight_load(a.q_weight, m), wk = weight_load(a.k_weight, m);
+  const double inv_d = 1.0 / D;
+  for (int64_t wave = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+       wave < grid.waves; wave += (int64_t)gridDim.x * 4) {
+    const RowTask t = row_task(wave, grid);
+    const RowAngles ang = row_angles(a, m, t.token);
+    // the values of group g in each lane; queries and keys differ in three numbers
+    const auto head_of = [&](int g) { return (g < grid.q_groups ? g : g - grid.q_groups) * N + sub; };
+    const auto on = [&](int g) { return head_of(g) < (g < grid.q_groups ? a.q_heads : a.k_heads); };
+    const auto load = [&](int g) {
+      return row_load((g < grid.q_groups ? a.q + t.token * a.q_stride : a.k + t.token * a.k_stride) +
+                          head_of(g) * D, m, on(g));
+    };
+    Row8 x = load(t.first);
+    for (int g = t.first; g < t.last; ++g) {
+      const Row8 next = load(g + 1 < t.last ? g + 1 : g);
+      const bool isq = g < grid.q_groups;
+      const Row8 y = row_norm_rope<LPH, PAIRS>(x, m, (isq ? a.q_weight : a.k_weight) != nullptr,
+                                               isq ? wq : wk, a.eps, inv_d, ang);
+      row_store((isq ? a.q_out + t.token * a.q_out_stride : a.k_out + t.token * a.k_out_stride) +
+                    head_of(g) * D, m, y, on(g));
+      x = next;
+    }
   }
 }
 
 template <int LPH>
 static hipError_t launch_fwd(const nvfp4_qk_args& a, hipStream_t s) {
-  const int per_token = (a.q_heads + a.k_heads + 64 / LPH - 1) / (64 / LPH);
-  const int64_t tasks = a.tokens * per_token;
+  const RowGrid g = row_grid_of(a.tokens, LPH, a.q_heads, a.k_heads, 0);
   if (a.pairs == NVFP4_PAIRS_HALVES)
-    hipLaunchKernelGGL((qk_norm_rope_kernel<LPH, NVFP4_PAIRS_HALVES>), dim3(row_grid(tasks)),
-                       dim3(kRowThreads), 0, s, a, tasks, per_token);
+    hipLaunchKernelGGL((qk_norm_rope_kernel<LPH, NVFP4_PAIRS_HALVES>), dim3(row_blocks(g)),
+                       dim3(kRowThreads), 0, s, a, g);
   else
-    hipLaunchKernelGGL((qk_norm_rope_kernel<LPH, NVFP4_PAIRS_NEIGHBOURS>), dim3(row_grid(tasks)),
-                       dim3(kRowThreads), 0, s, a, tasks, per_token);
+    hipLaunchKernelGGL((qk_norm_rope_kernel<LPH, NVFP4_PAIRS_NEIGHBOURS>), dim3(row_blocks(g)),
+                       dim3(kRowThreads), 0, s, a, g);
   return hipGetLastError();
 }
 
@@ -54,12 +61,15 @@ hipError_t launch_qk_norm_rope(const nvfp4_qk_args& a, hipStream_t s) {
 }
 
 // ---------------------------------------------------------------- gradient
-// Workspace: a counter, then one partial dw of D doubles per workgroup.
+// Workspace: arrival counters of the teams and of the whole launch (each on a
+// 128-byte line), then one partial (dq_weight, dk_weight) of D doubles each
+// per workgroup and one per team.
 constexpr int kBwdGroups = 1024;
-constexpr size_t kBwdHead = 256;
+constexpr int kBwdTeams = 32;
+constexpr size_t kBwdHead = 128 * (kBwdTeams + 1);
 
 size_t qk_norm_rope_bwd_workspace(int head_dim) {
-  return kBwdHead + (size_t)kBwdGroups * head_dim * sizeof(double);
+  return kBwdHead + (size_t)(kBwdGroups + kBwdTeams) * 2 * head_dim * sizeof(double);
 }
 
 struct BwdArgs {
@@ -68,135 +78,178 @@ struct BwdArgs {
   int64_t gq_stride, gk_stride;
   float *dqw, *dkw;
   uint8_t* ws;
-  int64_t q_tasks, k_tasks;
-  int q_per_token, k_per_token;
-  int q_groups, groups;  // workgroups [0, q_groups) take queries, the rest keys
+  RowGrid grid;
 };
 
-// Each workgroup takes query heads or key heads only, so that a lane keeps
-// one set of dw sums, in binary64, over all its rows; a workgroup's sums go
-// to its slot of the workspace and the last workgroup adds the slots in
-// order.
+// One head's gradient in the lane; g n is added to dw.
+template <int LPH, int PAIRS>
+__device__ __forceinline__ Row8 row_bwd(const Row8& in, const Row8& grad, const RowMap<LPH>& m, bool norm,
+                                        const Row8& weight, float eps, float inv_d,
+                                        const RowAngles& ang, float (&dw)[8]) {
+  float g[8];
+  grad.unpack(g);
+  if (m.rotated) row_rotate<PAIRS, -1>(g, ang);
+  if (norm) {
+    float x[8], w[8], ss = 0.0f;
+    in.unpack(x);
+    weight.unpack(w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(x[i], x[i], ss);
+    const float v = row_sum<LPH>(ss) * inv_d + eps;
+    const float r = __builtin_isinf(v) ? 0.0f : 1.0f / __builtin_sqrtf(v);
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i] *= r;  // n
+      dw[i] = __builtin_fmaf(g[i], x[i], dw[i]);
+      g[i] *= w[i];
+      dot = __builtin_fmaf(g[i], x[i], dot);
+    }
+    dot = row_sum<LPH>(dot) * inv_d;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = r * __builtin_fmaf(-x[i], dot, g[i]);
+  }
+  return Row8{make_uint2(bf16_pair(g[0], g[1]), bf16_pair(g[2], g[3])),
+              make_uint2(bf16_pair(g[4], g[5]), bf16_pair(g[6], g[7]))};
+}
+
+__device__ __forceinline__ void put64(double* p, double v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ double get64(const double* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Sum of slots first, first + step, ... < last of n doubles each, in the
+// threads e < n, in order (eight loads in flight).
+__device__ __forceinline__ double sum_slots(const double* slots, int n, int e, int first, int last, int step) {
+  double v = 0.0;
+  int i = first;
+  for (; i + 7 * step < last; i += 8 * step) {
+    double x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = get64(slots + (size_t)(i + k * step) * n + e);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v += x[k];
+  }
+  for (; i < last; i += step) v += get64(slots + (size_t)i * n + e);
+  return v;
+}
+
+// A wavefront walks tokens; over one token's heads the sums of dw stay in
+// binary32 (at most 1024 terms of one lane's column), over tokens in
+// binary64.  A workgroup's sums go to its slot; the last workgroup of each of
+// 32 teams adds the team's slots in order, the last team the teams' sums: no
+// atomic addition, the same bits on every run.  Slots are written and read at
+// the level that the whole GPU sees, so no cache is written back.
 template <int LPH, int PAIRS>
 __global__ void __launch_bounds__(kRowThreads)
 qk_norm_rope_bwd_kernel(BwdArgs b) {
-  __shared__ double part[4][256];
+  constexpr int N = 64 / LPH;
+  __shared__ double part[4][2 * 256];
   __shared__ bool last;
   const nvfp4_qk_args& a = b.a;
-  const int D = a.head_dim;
+  const RowGrid& grid = b.grid;
+  const int D = a.head_dim, sub = (int)(threadIdx.x & 63) / LPH, wv = threadIdx.x >> 6;
   const RowMap<LPH> m(D, a.rot_dim, PAIRS);
-  const bool isq = (int)blockIdx.x < b.q_groups;
-  const int group = isq ? blockIdx.x : blockIdx.x - b.q_groups;
-  const int groups = isq ? b.q_groups : b.groups - b.q_groups;
-  const int64_t tasks = isq ? b.q_tasks : b.k_tasks;
-  const int per_token = isq ? b.q_per_token : b.k_per_token;
-  const int heads = isq ? a.q_heads : a.k_heads;
-  const uint16_t* x = isq ? a.q : a.k;
-  const uint16_t* gy = isq ? b.gq : b.gk;
-  uint16_t* dx = isq ? a.q_out : a.k_out;
-  const int64_t xs = isq ? a.q_stride : a.k_stride, gs = isq ? b.gq_stride : b.gk_stride;
-  const int64_t ds = isq ? a.q_out_stride : a.k_out_stride;
-  const uint16_t* w = isq ? a.q_weight : a.k_weight;
+  const Row8 wq = weight_load(a.q_weight, m), wk = weight_load(a.k_weight, m);
   const float inv_d = 1.0f / (float)D, eps = a.eps;
-  float wf[8];
-  if (w) row_load(w, m, wf);
-  double dw[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  for (int64_t t0 = (int64_t)group * 4 + (threadIdx.x >> 6); t0 < tasks; t0 += (int64_t)groups * 4) {
-    const RowTask t = row_task<LPH>(t0, per_token);
-    RowMap<LPH> mm = m;
-    mm.active = m.active && t.head < heads;
-    const RowAngles g = row_angles(a, mm, t.token);
-    float xv[8], gv[8];
-    row_load(x + t.token * xs + (int64_t)t.head * D, mm, xv);
-    row_load(gy + t.token * gs + (int64_t)t.head * D, mm, gv);
-    if (mm.rotated) row_rotate<PAIRS, -1>(gv, g);
-    if (w) {
-      float ss = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(xv[i], xv[i], ss);
-      const float v = row_sum<LPH>(ss) * inv_d + eps;
-      const float r = __builtin_isinf(v) ? 0.0f : 1.0f / __builtin_sqrtf(v);
-      float dot = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        xv[i] *= r;  // n
-        if (mm.active) dw[i] += (double)(gv[i] * xv[i]);
-        gv[i] *= wf[i];
-        dot = __builtin_fmaf(gv[i], xv[i], dot);
+  double sum_q[8] = {}, sum_k[8] = {};
+  for (int64_t wave = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(wv); wave < grid.waves;
+       wave += (int64_t)gridDim.x * 4) {
+    const RowTask t = row_task(wave, grid);
+    const RowAngles ang = row_angles(a, m, t.token);
+    // the groups of one kind (queries, then keys): their sums of dw
+    const auto side = [&](const uint16_t* x, int64_t xs, const uint16_t* y, int64_t ys, uint16_t* d, int64_t ds,
+                          int heads, int g0, int g1, bool norm, const Row8& weight, double (&sum)[8]) {
+      if (g0 >= g1) return;
+      x += t.token * xs + sub * D;
+      y += t.token * ys + sub * D;
+      d += t.token * ds + sub * D;
+      const auto on = [&](int g) { return g * N + sub < heads; };
+      float dw[8] = {};
+      Row8 xv = row_load(x + g0 * N * D, m, on(g0)), yv = row_load(y + g0 * N * D, m, on(g0));
+      for (int g = g0; g < g1; ++g) {
+        const int gn = g + 1 < g1 ? g + 1 : g;
+        const Row8 xn = row_load(x + gn * N * D, m, on(gn)), yn = row_load(y + gn * N * D, m, on(gn));
+        row_store(d + g * N * D, m, row_bwd<LPH, PAIRS>(xv, yv, m, norm, weight, eps, inv_d, ang, dw), on(g));
+        xv = xn;
+        yv = yn;
       }
-      dot = row_sum<LPH>(dot) * inv_d;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) gv[i] = r * __builtin_fmaf(-xv[i], dot, gv[i]);
-    }
-    row_store(dx + t.token * ds + (int64_t)t.head * D, mm,
-              make_uint2(bf16_pair(gv[0], gv[1]), bf16_pair(gv[2], gv[3])),
-              make_uint2(bf16_pair(gv[4], gv[5]), bf16_pair(gv[6], gv[7])));
+      for (int i = 0; i < 8; ++i) sum[i] += dw[i];
+    };
+    const int q1 = t.last < grid.q_groups ? t.last : grid.q_groups;
+    const int k0 = (t.first > grid.q_groups ? t.first : grid.q_groups) - grid.q_groups;
+    side(a.q, a.q_stride, b.gq, b.gq_stride, a.q_out, a.q_out_stride, a.q_heads, t.first, q1,
+         a.q_weight != nullptr, wq, sum_q);
+    side(a.k, a.k_stride, b.gk, b.gk_stride, a.k_out, a.k_out_stride, a.k_heads, k0, t.last - grid.q_groups,
+         a.k_weight != nullptr, wk, sum_k);
   }
   if (!b.dqw && !b.dkw) return;
   // the wavefront's heads, then the workgroup's wavefronts
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    for (int d = LPH; d < 64; d <<= 1) dw[i] += __shfl_xor(dw[i], d);
+    for (int d = LPH; d < 64; d <<= 1) {
+      sum_q[i] += __shfl_xor(sum_q[i], d);
+      sum_k[i] += __shfl_xor(sum_k[i], d);
+    }
   if ((threadIdx.x & 63) < LPH && m.active) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      part[threadIdx.x >> 6][m.e0 + i] = dw[i];
-      part[threadIdx.x >> 6][m.e1 + i] = dw[4 + i];
+      part[wv][m.e0 + i] = sum_q[i];
+      part[wv][m.e1 + i] = sum_q[4 + i];
+      part[wv][D + m.e0 + i] = sum_k[i];
+      part[wv][D + m.e1 + i] = sum_k[4 + i];
     }
   }
   __syncthreads();
+  const int n = 2 * D, G = gridDim.x;
   double* slots = reinterpret_cast<double*>(b.ws + kBwdHead);
-  uint32_t* counter = reinterpret_cast<uint32_t*>(b.ws);
-  if ((int)threadIdx.x < D) {
-    const int e = threadIdx.x;
-    const double v = (part[0][e] + part[1][e]) + (part[2][e] + part[3][e]);
-    __hip_atomic_store(&slots[(size_t)blockIdx.x * D + e], v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
-  // the slot has reached the coherent level before the workgroup arrives
-  __threadfence();
+  double* team_slots = slots + (size_t)kBwdGroups * n;
+  for (int e = threadIdx.x; e < n; e += kRowThreads)
+    put64(slots + (size_t)blockIdx.x * n + e, (part[0][e] + part[1][e]) + (part[2][e] + part[3][e]));
+  // arrive once the slot has reached the level that all see
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
-  if (threadIdx.x == 0)
-    last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
-           (uint32_t)b.groups - 1;
+  const int teams = G < kBwdTeams ? G : kBwdTeams, team = blockIdx.x % teams;
+  const uint32_t members = (uint32_t)((G - team + teams - 1) / teams);
+  if (threadIdx.x == 0) {
+    uint32_t* c = reinterpret_cast<uint32_t*>(b.ws + 128 * (1 + team));
+    last = __hip_atomic_fetch_add(c, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == members - 1;
+    if (last) __hip_atomic_store(c, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
   __syncthreads();
   if (!last) return;
-  if (threadIdx.x == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  if ((int)threadIdx.x < D) {
-    for (int kind = 0; kind < 2; ++kind) {
-      float* out = kind == 0 ? b.dqw : b.dkw;
-      if (!out) continue;
-      double v = 0.0;
-      for (int i = kind == 0 ? 0 : b.q_groups; i < (kind == 0 ? b.q_groups : b.groups); ++i)
-        v += __hip_atomic_load(&slots[(size_t)i * D + threadIdx.x], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      out[threadIdx.x] = (float)v;
-    }
+  for (int e = threadIdx.x; e < n; e += kRowThreads)
+    put64(team_slots + (size_t)team * n + e, sum_slots(slots, n, e, team, G, teams));
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    uint32_t* c = reinterpret_cast<uint32_t*>(b.ws);
+    last = __hip_atomic_fetch_add(c, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)teams - 1;
+    if (last) __hip_atomic_store(c, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  if (!last) return;
+  for (int e = threadIdx.x; e < n; e += kRowThreads) {
+    float* out = e < D ? b.dqw : b.dkw;
+    if (out) out[e < D ? e : e - D] = (float)sum_slots(team_slots, n, e, 0, teams, 1);
   }
 }
 
 template <int LPH>
 static hipError_t launch_bwd(BwdArgs b, hipStream_t s) {
-  const int per = 64 / LPH;
-  b.q_per_token = (b.a.q_heads + per - 1) / per;
-  b.k_per_token = (b.a.k_heads + per - 1) / per;
-  b.q_tasks = b.a.tokens * b.q_per_token;
-  b.k_tasks = b.a.tokens * b.k_per_token;
-  // workgroups in proportion to the tasks, at least one for each side that
-  // has heads, at most the workspace's slots
-  auto wgs = [](int64_t tasks, int64_t cap) {
-    const int64_t g = (tasks + 3) / 4;
-    return (int)(g < cap ? g : cap);
-  };
-  const int64_t all = b.q_tasks + b.k_tasks;
-  int64_t qcap = all ? (int64_t)((double)kBwdGroups * (double)b.q_tasks / (double)all) : 0;
-  qcap = qcap < 1 ? 1 : qcap > kBwdGroups - 1 ? kBwdGroups - 1 : qcap;
-  b.q_groups = b.a.q_heads ? (b.q_tasks ? wgs(b.q_tasks, qcap) : 1) : 0;
-  b.groups = b.q_groups + (b.a.k_heads ? (b.k_tasks ? wgs(b.k_tasks, kBwdGroups - qcap) : 1) : 0);
+  b.grid = row_grid_of(b.a.tokens, LPH, b.a.q_heads, b.a.k_heads, 0);
+  // with no tokens one workgroup writes the zero gradients of the weights
+  int64_t blocks = (b.grid.waves + 3) / 4;
+  blocks = blocks < 1 ? 1 : blocks < kBwdGroups ? blocks : kBwdGroups;
   if (b.a.pairs == NVFP4_PAIRS_HALVES)
-    hipLaunchKernelGGL((qk_norm_rope_bwd_kernel<LPH, NVFP4_PAIRS_HALVES>), dim3((unsigned)b.groups),
+    hipLaunchKernelGGL((qk_norm_rope_bwd_kernel<LPH, NVFP4_PAIRS_HALVES>), dim3((unsigned)blocks),
                        dim3(kRowThreads), 0, s, b);
   else
-    hipLaunchKernelGGL((qk_norm_rope_bwd_kernel<LPH, NVFP4_PAIRS_NEIGHBOURS>),
-                       dim3((unsigned)b.groups), dim3(kRowThreads), 0, s, b);
+    hipLaunchKernelGGL((qk_norm_rope_bwd_kernel<LPH, NVFP4_PAIRS_NEIGHBOURS>), dim3((unsigned)blocks),
+                       dim3(kRowThreads), 0, s, b);
   return hipGetLastError();
 }
 

@@ -42,23 +42,30 @@ struct RowMap {
   }
 };
 
-template <int LPH>
-__device__ __forceinline__ void row_load(const uint16_t* p, const RowMap<LPH>& m, float (&x)[8]) {
-  uint2 a = make_uint2(0, 0), b = make_uint2(0, 0);
-  if (m.active) {
-    a = *reinterpret_cast<const uint2*>(p + m.e0);
-    b = *reinterpret_cast<const uint2*>(p + m.e1);
+// The lane's eight values as bf16 patterns: group 0 and group 1.
+struct Row8 {
+  uint2 a, b;
+  __device__ __forceinline__ void unpack(float (&x)[8]) const {
+    x[0] = bf16_lo(a.x); x[1] = bf16_hi(a.x); x[2] = bf16_lo(a.y); x[3] = bf16_hi(a.y);
+    x[4] = bf16_lo(b.x); x[5] = bf16_hi(b.x); x[6] = bf16_lo(b.y); x[7] = bf16_hi(b.y);
   }
-  x[0] = bf16_lo(a.x); x[1] = bf16_hi(a.x); x[2] = bf16_lo(a.y); x[3] = bf16_hi(a.y);
-  x[4] = bf16_lo(b.x); x[5] = bf16_hi(b.x); x[6] = bf16_lo(b.y); x[7] = bf16_hi(b.y);
+};
+
+template <int LPH>
+__device__ __forceinline__ Row8 row_load(const uint16_t* p, const RowMap<LPH>& m, bool on = true) {
+  Row8 r = {make_uint2(0, 0), make_uint2(0, 0)};
+  if (m.active && on) {
+    r.a = *reinterpret_cast<const uint2*>(p + m.e0);
+    r.b = *reinterpret_cast<const uint2*>(p + m.e1);
+  }
+  return r;
 }
 
 template <int LPH>
-__device__ __forceinline__ void row_store(uint16_t* p, const RowMap<LPH>& m, const uint2& a,
-                                          const uint2& b) {
-  if (m.active) {
-    *reinterpret_cast<uint2*>(p + m.e0) = a;
-    *reinterpret_cast<uint2*>(p + m.e1) = b;
+__device__ __forceinline__ void row_store(uint16_t* p, const RowMap<LPH>& m, const Row8& r, bool on = true) {
+  if (m.active && on) {
+    *reinterpret_cast<uint2*>(p + m.e0) = r.a;
+    *reinterpret_cast<uint2*>(p + m.e1) = r.b;
   }
 }
 
@@ -149,59 +156,84 @@ __device__ __forceinline__ double rsqrt64(double a) {
   return __builtin_isinf(a) ? 0.0 : y;
 }
 
-// Norm (w not null) and rotation of the lane's values: bf16 patterns of
+// Norm (with a weight) and rotation of the lane's values: bf16 patterns of
 // group 0 and group 1.  binary64 throughout: the result is the formula's
 // rounded once (up to 2^-50 before the rounding), whatever the sum's order,
 // so that a key lands on the formula's side of the 4-bit borders behind it.
+// gfx950 runs binary64 fused multiply-adds at the rate of unpacked binary32
+// ones, so the pass stays bound by memory.
 template <int LPH, int PAIRS>
-__device__ __forceinline__ void row_norm_rope(const float (&x)[8], const RowMap<LPH>& m,
-                                              const uint16_t* w, double eps, double inv_d,
-                                              const RowAngles& g, uint2& o0, uint2& o1) {
+__device__ __forceinline__ Row8 row_norm_rope(const Row8& in, const RowMap<LPH>& m, bool norm,
+                                              const Row8& weight, double eps, double inv_d,
+                                              const RowAngles& g) {
+  float x[8];
+  in.unpack(x);
   double y[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) y[i] = (double)x[i];
-  if (w) {
+  if (norm) {
     double ss = 0.0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) ss = __builtin_fma(y[i], y[i], ss);
     const double r = rsqrt64(row_sum<LPH>(ss) * inv_d + eps);
-    float wf[8];
-    row_load(w, m, wf);
+    weight.unpack(x);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = y[i] * r * (double)wf[i];
+    for (int i = 0; i < 8; ++i) y[i] = y[i] * r * (double)x[i];
   }
   if (m.rotated) row_rotate<PAIRS, 1>(y, g);
-  o0 = make_uint2(bf16_pair((float)y[0], (float)y[1]), bf16_pair((float)y[2], (float)y[3]));
-  o1 = make_uint2(bf16_pair((float)y[4], (float)y[5]), bf16_pair((float)y[6], (float)y[7]));
+  return Row8{make_uint2(bf16_pair((float)y[0], (float)y[1]), bf16_pair((float)y[2], (float)y[3])),
+              make_uint2(bf16_pair((float)y[4], (float)y[5]), bf16_pair((float)y[6], (float)y[7]))};
 }
 
-// The wavefront's task: a token and the first of 64 / LPH consecutive heads.
+// The lane's part of a weight; zeros without one.
+template <int LPH>
+__device__ __forceinline__ Row8 weight_load(const uint16_t* w, const RowMap<LPH>& m) {
+  return row_load(w, m, w != nullptr);
+}
+
+// A wavefront takes one token and a run of its head groups (64 / LPH heads
+// each; the groups of queries, then of keys, then of values, so that a group
+// is of one kind).  Its angles and weights are loaded once and stay in
+// registers.
+struct RowGrid {
+  int q_groups, k_groups, v_groups;
+  int per_wave;  // groups a wavefront takes
+  int parts;     // wavefronts a token takes
+  int64_t waves;
+};
+// Enough wavefronts to fill the card (256 CUs x 32) come first, long runs
+// second: a token is cut up only where there are few tokens.
+inline RowGrid row_grid_of(int64_t tokens, int lph, int q_heads, int k_heads, int v_heads) {
+  const int n = 64 / lph;
+  RowGrid g = {(q_heads + n - 1) / n, (k_heads + n - 1) / n, (v_heads + n - 1) / n, 1, 1, 0};
+  const int groups = g.q_groups + g.k_groups + g.v_groups;
+  const int64_t want = (int64_t)device_cu_count() * 32;
+  int64_t parts = tokens > 0 ? (want + tokens - 1) / tokens : 1;
+  parts = parts < groups ? parts : groups;
+  g.per_wave = (int)((groups + parts - 1) / parts);
+  g.parts = (groups + g.per_wave - 1) / g.per_wave;
+  g.waves = tokens * g.parts;
+  return g;
+}
+inline unsigned row_blocks(const RowGrid& g) {
+  const int64_t n = (g.waves + 3) / 4, cap = (int64_t)1 << 30;
+  return (unsigned)(n < cap ? n : cap);
+}
+
 struct RowTask {
   int64_t token;
-  int head;
+  int first, last;  // groups [first, last)
 };
-template <int LPH>
-__device__ __forceinline__ RowTask row_task(int64_t wave, int per_token) {
-  RowTask t;
-  uint32_t part;
-  if ((uint64_t)wave >> 32) {
-    t.token = wave / per_token;
-    part = (uint32_t)(wave - t.token * per_token);
-  } else {
-    t.token = (uint32_t)wave / (uint32_t)per_token;
-    part = (uint32_t)wave - (uint32_t)t.token * (uint32_t)per_token;
-  }
-  t.head = (int)part * (64 / LPH) + (int)((threadIdx.x & 63) / LPH);
-  return t;
+// A token is cut up only where there are fewer tokens than wavefronts on the
+// card, so the division is one of 32 bits.
+__device__ __forceinline__ RowTask row_task(int64_t wave, const RowGrid& g) {
+  const uint32_t cut = g.parts == 1 ? 0u : (uint32_t)wave / (uint32_t)g.parts;
+  const int part = g.parts == 1 ? 0 : (int)((uint32_t)wave - cut * (uint32_t)g.parts);
+  const int groups = g.q_groups + g.k_groups + g.v_groups;
+  const int first = part * g.per_wave, end = first + g.per_wave;
+  return RowTask{g.parts == 1 ? wave : (int64_t)cut, first, end < groups ? end : groups};
 }
 
 inline int lanes_per_head(int D) { return D <= 32 ? 4 : D <= 64 ? 8 : D <= 128 ? 16 : 32; }
-
-// Workgroups for `tasks` wavefront tasks, four a workgroup; the kernels loop
-// where there are more than the grid holds.
-inline unsigned row_grid(int64_t tasks) {
-  const int64_t g = (tasks + 3) / 4, cap = (int64_t)1 << 30;
-  return (unsigned)(g < cap ? g : cap);
-}
 
 }  // namespace nvfp4

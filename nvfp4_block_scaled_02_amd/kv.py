@@ -296,7 +296,7 @@ def qk_norm_rope_bwd(dq_out: Optional[torch.Tensor], dk_out: Optional[torch.Tens
             _need(workspace, torch.uint8, "workspace", n)
             ws = workspace
         else:
-            ws = _cached_workspace(_BWD_WORKSPACES, dev, n, 256)
+            ws = _cached_workspace(_BWD_WORKSPACES, dev, n, n)
     _invoke("nvfp4_qk_norm_rope_bwd",
             (ctypes.byref(a), _ptr(dq_out), strides[0], _ptr(dk_out), strides[1], _ptr(dws[0]),
              _ptr(dws[1]), _ptr(ws)), dev,
