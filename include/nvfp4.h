@@ -692,19 +692,17 @@ int nvfp4_kv_read(const nvfp4_kv_cache* cache, const int64_t* slots, int64_t tok
  *   max_seq_len  an upper bound of seq_lens that sizes the launch (longer
  *             requests are still computed in full).
  *   workspace nvfp4_kv_attention_workspace_bytes(args) bytes, 16-byte
- *             aligned, whose first NVFP4_KV_ATTENTION_COUNTER_BYTES are zero
- *             before its first use (every completed call leaves them zero);
- *             may be NULL where that size is 0.  Overlapping calls need their
- *             own.  The bytes depend on tokens, batch, max_seq_len, heads and
- *             D alone.
+ *             aligned, with any contents; may be NULL where that size is 0.
+ *             Overlapping calls need their own.  The bytes depend on tokens,
+ *             batch, max_seq_len, heads, D, window and whether cu_q is given.
+ * At most two launches: long key ranges are split over workgroups, and a
+ * second launch joins the pieces in order.
  * Errors (NVFP4_ERR_INVALID): the cache's rules, NULL or misaligned pointers,
  * sizes < 0, q_heads not a positive multiple of kv_heads or above
  * NVFP4_KV_MAX_HEADS, cu_q NULL with tokens != batch, scale not finite,
  * window < 0, batch, tokens, table_width or max_seq_len > 2^31 - 1;
- * NVFP4_ERR_UNSUPPORTED: table_width * page_size > 2^30.
+ * NVFP4_ERR_UNSUPPORTED: table_width * page_size > 2^30 or tokens * q_heads > 2^31.
  */
-#define NVFP4_KV_ATTENTION_COUNTER_BYTES 65536
-
 typedef struct nvfp4_kv_attention_args {
   const uint16_t* q;
   int64_t tokens, q_stride;

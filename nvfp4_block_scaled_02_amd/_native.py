@@ -38,7 +38,6 @@ class QuantArgs(ctypes.Structure):
 
 
 PAIRS_HALVES, PAIRS_NEIGHBOURS = 0, 1
-KV_ATTENTION_COUNTER_BYTES = 65536  # NVFP4_KV_ATTENTION_COUNTER_BYTES of include/nvfp4.h
 
 
 class KVCacheArgs(ctypes.Structure):

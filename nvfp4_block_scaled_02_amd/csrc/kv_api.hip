@@ -166,8 +166,10 @@ static int attention_ok(const nvfp4_kv_attention_args& a) {
     return NVFP4_ERR_INVALID;
   if (!a.cu_q && a.tokens != a.batch) return NVFP4_ERR_INVALID;
   if (!isfinite(a.scale)) return NVFP4_ERR_INVALID;
-  // key positions, and their sums with a tile's width, stay in 32 bits
-  if (st == NVFP4_OK && a.table_width > ((int64_t)1 << 30) / a.cache.page_size) return NVFP4_ERR_UNSUPPORTED;
+  // key positions, and their sums with a tile's width, and rows stay in 32 bits
+  if (st == NVFP4_OK && (a.table_width > ((int64_t)1 << 30) / a.cache.page_size ||
+                         a.tokens > ((int64_t)1 << 31) / a.q_heads))
+    return NVFP4_ERR_UNSUPPORTED;
   return st;
 }
 

@@ -25,10 +25,12 @@
 //
 // Few rows (decoding, drafted tokens): the four wavefronts of a workgroup
 // take every fourth tile and join through LDS, and long key ranges are split
-// over workgroups whose partial results (binary32) meet in the workspace; the
-// last workgroup to arrive joins them in order.  Many rows (prompts): each
+// over workgroups whose partial results (binary32) a second launch joins in
+// order.  Many rows (prompts): each
 // wavefront has rows of its own, and the workgroup dequantizes each block of
 // keys once, into LDS.
+#include <math.h>
+
 #include "kv.hpp"
 
 namespace nvfp4 {
@@ -38,7 +40,6 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kAttnThreads = 256;
 constexpr int kMaxSplits = 128;
-constexpr int kMaxGroups = NVFP4_KV_ATTENTION_COUNTER_BYTES / 4;
 constexpr int kSlabStride = 68;  // floats of a 64-column slab row: 4 apart in the banks
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -120,17 +121,12 @@ struct Reader {
   const int32_t* table;  // of the request
   int last;              // last table entry that may be read
   int shift, kvh, r, g;
+  // Always a vector load (one line, all lanes): loads return in order, so it
+  // goes ahead of the tile loads it will be used after.  A scalar load where a
+  // tile lies in one page made the compiler wait for every load in flight.
   __device__ __forceinline__ Pages pages(int tile0) const {
-    Pages p;
-    if (shift >= 5) {  // the tile lies in one page: a scalar load
-      const int i = tile0 >> shift;
-      p.k = p.v = table[i < last ? i : last];
-    } else {
-      const int ik = (tile0 + 8 * (r >> 2)) >> shift, iv = (tile0 + 8 * g) >> shift;
-      p.k = table[ik < last ? ik : last];
-      p.v = table[iv < last ? iv : last];
-    }
-    return p;
+    const int ik = (tile0 + 8 * (r >> 2)) >> shift, iv = (tile0 + 8 * g) >> shift;
+    return Pages{table[ik < last ? ik : last], table[iv < last ? iv : last]};
   }
   // Codes and scales of one 16-key product (t of the tile): D / 8 bytes and D /
   // 64 scale bytes of the lane's key.
@@ -221,80 +217,78 @@ __device__ __forceinline__ uint64_t keys_in(int key0, int lo, int hi, bool ok) {
 // carries into the next: 0x7F + 1).
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t s) { return ((s & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 
-// Row of a request -> its token among the request's, and its head in the group.
-__device__ __forceinline__ int64_t split_row(int64_t row, int group, int64_t& head) {
-  const uint32_t r = (uint32_t)row;
-  if ((uint64_t)row >> 32) {
-    const int64_t t = row / group;
-    head = row - t * group;
-    return t;
-  }
-  head = r % (uint32_t)group;
-  return r / (uint32_t)group;
-}
-
 // A workgroup's place: its request and rows.
+// Rows (token x head of a group) and positions stay in 32 bits: the entry point
+// refuses more than 2^31 rows and 2^30 keys a request.
 struct Place {
-  int64_t b;           // request (batch: rows that belong to none)
-  int64_t begin, end;  // its rows of q
-  int64_t row0;        // first row (token x head of the group) of the workgroup
-  int count;           // rows of the workgroup; 0: nothing to do
-  int len;             // keys [0, len)
-  int64_t pos0;        // position of the request's first query
-  __device__ __forceinline__ void bounds(const nvfp4_kv_attention_args& a, int group, int64_t row, int& lo,
-                                         int& hi) const {
-    int64_t head;
-    const int64_t p = pos0 + split_row(row, group, head);
-    const int64_t h = a.causal && p + 1 < len ? p + 1 : len;
-    const int64_t w = a.window > 0 ? p - a.window + 1 : 0;
-    hi = (int)(h < 0 ? 0 : h);
-    lo = (int)(w < 0 ? 0 : w > len ? len : w);
-  }
+  int b;           // request (batch: rows that belong to none)
+  int begin, end;  // its rows of q
+  int row0;        // first row of the workgroup, in the request
+  int count;       // rows of the workgroup; 0: nothing to do
+  int len;         // keys [0, len)
+  int pos0;        // position of the request's first query
 };
+
+// Keys that a row attends, [lo, hi).  Both ascend with the row.
+__device__ __forceinline__ void bounds_of(const AttnArgs& args, const Place& at, int row, int& lo, int& hi) {
+  const nvfp4_kv_attention_args& a = args.a;
+  const int64_t p = (int64_t)at.pos0 + (uint32_t)row / (uint32_t)args.group;
+  const int64_t h = a.causal && p + 1 < at.len ? p + 1 : at.len;
+  const int64_t w = a.window > 0 ? p - a.window + 1 : 0;
+  hi = (int)(h < 0 ? 0 : h);
+  lo = (int)(w < 0 ? 0 : w > at.len ? at.len : w);
+}
 
 __device__ __forceinline__ Place place_of(const AttnArgs& args, uint32_t tile, int lane) {
   const nvfp4_kv_attention_args& a = args.a;
   Place p;
-  int64_t local;
+  int local;
   p.count = 0;
   if (!a.cu_q) {
-    p.b = tile / args.tiles_per_request;
-    local = tile - (uint32_t)p.b * args.tiles_per_request;
+    p.b = (int)(tile / args.tiles_per_request);
+    local = (int)(tile - (uint32_t)p.b * args.tiles_per_request);
     p.begin = p.b;
     p.end = p.b + 1;
   } else {
     // request b's tiles begin at floor(cu_q[b] * group / rows) + b; rows past
     // cu_q[batch] count as a request of length 0.  64 probes at a time.
-    const auto cu = [&](int64_t i) {
-      const int64_t v = a.cu_q[i];
-      return v < 0 ? 0 : v < a.tokens ? v : a.tokens;
+    const int tokens = (int)a.tokens, batch = (int)a.batch;
+    const auto cu = [&](int i) {
+      const int v = a.cu_q[i];
+      return v < 0 ? 0 : v < tokens ? v : tokens;
     };
-    const auto start = [&](int64_t i) { return (uint64_t)cu(i) * (uint32_t)args.group / (uint32_t)args.rows + i; };
-    int64_t lo = 0, n = a.batch + 1;
+    const auto start = [&](int i) { return (uint32_t)cu(i) * (uint32_t)args.group / (uint32_t)args.rows + (uint32_t)i; };
+    int lo = 0, n = batch + 1;
     while (n > 1) {
-      const int64_t step = (n + 63) / 64, i = lane * step;
+      const int step = (n - 1) / 64 + 1, i = lane * step;
       const bool before = i < n && start(lo + i) <= tile;
       const int hits = __popcll(__ballot(before));
-      const int64_t k = hits > 0 ? hits - 1 : 0;
+      const int k = hits > 0 ? hits - 1 : 0;
       lo += k * step;
       n = n - k * step < step ? n - k * step : step;
     }
-    p.b = lo;
-    local = (int64_t)tile - (int64_t)start(lo);
+    p.b = __builtin_amdgcn_readfirstlane(lo);
+    local = (int)(tile - start(p.b));
     if (local < 0) return p;
-    p.begin = cu(lo);
-    p.end = lo < a.batch ? cu(lo + 1) : a.tokens;
+    p.begin = cu(p.b);
+    p.end = p.b < batch ? cu(p.b + 1) : tokens;
     p.end = p.end < p.begin ? p.begin : p.end;
   }
-  const int64_t rows = (p.end - p.begin) * args.group;
-  p.row0 = local * args.rows;
-  if (p.row0 >= rows) return p;
-  p.count = (int)(rows - p.row0 < args.rows ? rows - p.row0 : args.rows);
-  const int64_t seq = p.b < a.batch ? a.seq_lens[p.b] : 0;
-  const int64_t room = a.table_width << args.shift;
-  p.len = (int)(seq < 0 ? 0 : seq < room ? seq : room);
+  const uint32_t rows = (uint32_t)(p.end - p.begin) * (uint32_t)args.group, row0 = (uint32_t)local * (uint32_t)args.rows;
+  if (row0 >= rows) return p;
+  p.row0 = (int)row0;
+  p.count = rows - row0 < (uint32_t)args.rows ? (int)(rows - row0) : args.rows;
+  const int seq = p.b < (int)a.batch ? a.seq_lens[p.b] : 0;
+  const int room = (int)a.table_width << args.shift;
+  p.len = seq < 0 ? 0 : seq < room ? seq : room;
   p.pos0 = seq - (p.end - p.begin);
   return p;
+}
+
+// Row of out (token * q_heads + head) of a workgroup's row.
+__device__ __forceinline__ int64_t out_row(const AttnArgs& args, const Place& at, int kvh, int row) {
+  const uint32_t rr = (uint32_t)(at.row0 + row), token = rr / (uint32_t)args.group;
+  return (int64_t)(at.begin + (int)token) * args.a.q_heads + kvh * args.group + (int)(rr - token * (uint32_t)args.group);
 }
 
 // ---------------------------------------------------------------- one tile
@@ -384,27 +378,36 @@ struct Walk {
     return p;
   }
 
-  // Query rows [first, first + 16 NQ) of the workgroup's `count` (the spare
-  // ones repeat the last) into binary16, each scaled by a power of two.
-  template <class RowAt, class Bounds>
-  __device__ __forceinline__ void start(const nvfp4_kv_attention_args& a, int group, int kvh, int first, int count,
-                                        int r, int g, const RowAt& row_at, const Bounds& bounds,
-                                        int64_t begin) {
+  // Query rows [first, first + 16 NQ) of the workgroup (the spare ones repeat
+  // the last one): their bf16 patterns as they lie in memory ...
+  struct RawQ {
+    uint4 x[NQ][NCH];
+  };
+  __device__ __forceinline__ void load_queries(const AttnArgs& args, const Place& at, int kvh, int first, int r, int g,
+                                               RawQ& raw) {
+    const nvfp4_kv_attention_args& a = args.a;
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
       int row = first + 16 * n + r;
-      row = row < count ? row : count - 1;
-      const int64_t rr = row_at(row);
-      bounds(rr, lo[n], hi[n]);
-      int64_t head;
-      const int64_t token = split_row(rr, group, head);
-      const uint16_t* src = a.q + (begin + token) * a.q_stride + ((int64_t)kvh * group + head) * D + g * (D / 4);
-      uint4 raw[NCH];
+      row = at.row0 + (row < at.count ? row : at.count - 1);
+      bounds_of(args, at, row, lo[n], hi[n]);
+      const uint32_t token = (uint32_t)row / (uint32_t)args.group;
+      const int head = kvh * args.group + (int)((uint32_t)row - token * (uint32_t)args.group);
+      const uint16_t* src = a.q + (int64_t)(at.begin + (int)token) * a.q_stride + head * D + g * (D / 4);
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) raw.x[n][i] = *reinterpret_cast<const uint4*>(src + 8 * i);
+    }
+  }
+  // ... and in binary16, each row scaled by a power of two.
+  __device__ __forceinline__ void start(const AttnArgs& args, int kvh, const RawQ& raw) {
+    const nvfp4_kv_attention_args& a = args.a;
+    const float common = outer_alpha(a.cache.k_amax[kvh], a.cache.global_fp8_max) * __builtin_fabsf(a.scale) * kLog2e;
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
       uint32_t top = 0;
 #pragma unroll
       for (int i = 0; i < NCH; ++i) {
-        raw[i] = *reinterpret_cast<const uint4*>(src + 8 * i);
-        const uint32_t t = chunk_abs_max_bits(raw[i]);
+        const uint32_t t = chunk_abs_max_bits(raw.x[n][i]);
         top = top > t ? top : t;
       }
       // the row's largest magnitude: bf16 patterns order like their values
@@ -417,15 +420,14 @@ struct Walk {
       const float up = __builtin_copysignf(__uint_as_float((uint32_t)e << 23), a.scale);
 #pragma unroll
       for (int i = 0; i < NCH; ++i) {
-        const uint32_t x[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        const uint32_t x[4] = {raw.x[n][i].x, raw.x[n][i].y, raw.x[n][i].z, raw.x[n][i].w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           q[n][i][2 * k] = (_Float16)(bf16_lo(x[k]) * up);
           q[n][i][2 * k + 1] = (_Float16)(bf16_hi(x[k]) * up);
         }
       }
-      factor[n] = __builtin_ldexpf(outer_alpha(a.cache.k_amax[kvh], a.cache.global_fp8_max) *
-                                       __builtin_fabsf(a.scale) * kLog2e, 127 - e);
+      factor[n] = __builtin_ldexpf(common, 127 - e);
       // a score of -inf stays below every other one
       factor[n] = factor[n] == 0.0f ? 0x1p-126f : factor[n];
       m[n] = thr[n] = -__builtin_inff();
@@ -434,6 +436,19 @@ struct Walk {
       for (int j = 0; j < NJ; ++j)
 #pragma unroll
         for (int e2 = 0; e2 < 4; ++e2) o[n][j][e2] = f32x4{0, 0, 0, 0};
+    }
+  }
+
+  // No key seen.
+  __device__ __forceinline__ void none() {
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      m[n] = -__builtin_inff();
+      l[n] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][j][e] = f32x4{0, 0, 0, 0};
     }
   }
 
@@ -475,17 +490,32 @@ struct Walk {
 };
 
 // ---------------------------------------------------------------- workspace
-// Partial results of a split tile: per (tile, head) group and split, rows x
-// (D values, then maximum and sum), written and read where the whole GPU sees
-// them (no cache holds a stale copy).
-__device__ __forceinline__ void put2(float* p, float a, float b) {
-  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), (uint64_t)u32(b) << 32 | u32(a), __ATOMIC_RELAXED,
-                     __HIP_MEMORY_SCOPE_AGENT);
+// Partial results of split tiles: per (tile, head) group and split, rows x D
+// accumulated values, and behind all of those a (maximum, sum) pair per row.
+struct Parts {
+  float* o;
+  float2* ml;
+};
+template <int D, int RW>
+__device__ __forceinline__ Parts parts_of(const AttnArgs& args, uint32_t tile, uint32_t kvh) {
+  const uint64_t first = ((uint64_t)tile * (uint32_t)args.a.cache.kv_heads + kvh) * (uint32_t)args.splits * RW;
+  const uint64_t all = (uint64_t)args.tiles * (uint32_t)args.a.cache.kv_heads * (uint32_t)args.splits * RW;
+  float* o = static_cast<float*>(args.a.workspace);
+  return Parts{o + first * D, reinterpret_cast<float2*>(o + all * D) + first};
 }
-__device__ __forceinline__ float2 get2(const float* p) {
-  const uint64_t v = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED,
-                                       __HIP_MEMORY_SCOPE_AGENT);
-  return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+
+// How the keys [k0, k1) of a tile are cut up: `n` pieces of `each`.
+struct Cut {
+  int n, each;
+};
+__device__ __forceinline__ Cut cut_of(const AttnArgs& args, int k0, int k1) {
+  if (args.splits == 1) return Cut{1, 0};
+  const int keys = k1 > k0 ? k1 - k0 : 0;
+  int n = (keys + args.chunk - 1) / args.chunk;
+  n = n < 1 ? 1 : n < args.splits ? n : args.splits;
+  const int each = ((keys + n - 1) / n + 127) & ~127;
+  n = each > 0 ? (keys + each - 1) / each : 1;
+  return Cut{n < 1 ? 1 : n, each};
 }
 
 // weight of a partial result with maximum m under the joint maximum M
@@ -499,11 +529,16 @@ constexpr int attn_waves(int D, int NQ) {
   return D * NQ <= 64 ? 4 : D * NQ <= 128 ? 3 : D * NQ <= 256 ? 2 : 1;
 }
 
+// Most 16-row tiles of a wavefront of the kernel below.  Four of D = 128 spill
+// and leave one wavefront a SIMD: 64 rows of 8 requests over up to 8192 keys
+// take 97 us that way and 44 us as two tiles of 32.
+constexpr int keys_nq_most(int D) { return D == 64 ? 4 : 2; }
+
 // Few rows: the wavefronts of a workgroup take every fourth key tile.
 template <int D, int NQ>
 __global__ void __launch_bounds__(kAttnThreads, attn_waves(D, NQ))
 kv_attention_keys_kernel(AttnArgs args) {
-  constexpr int NJ = D / 64, RW = 16 * NQ;
+  constexpr int NJ = D / 64, RW = 16 * NQ, SLOTS = 2;
   const nvfp4_kv_attention_args& a = args.a;
   const nvfp4_kv_cache& c = a.cache;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
@@ -517,65 +552,70 @@ kv_attention_keys_kernel(AttnArgs args) {
   const Place at_ = place_of(args, tile, lane);
   if (at_.count == 0) return;
   const int count = at_.count;
-  const auto bounds = [&](int64_t row, int& lo, int& hi) { at_.bounds(a, args.group, row, lo, hi); };
-  // keys that any row attends, and those that all attend: bounds ascend with the row
+  // keys that any row attends, and those that all attend
   int lo_any, hi_any, lo_all, hi_all;
-  bounds(at_.row0, lo_any, hi_all);
-  bounds(at_.row0 + count - 1, lo_all, hi_any);
+  bounds_of(args, at_, at_.row0, lo_any, hi_all);
+  bounds_of(args, at_, at_.row0 + count - 1, lo_all, hi_any);
   // this workgroup's share
-  int k0 = lo_any & ~31, k1 = hi_any, nsplit = 1;
-  if (args.splits > 1) {
-    const int keys = k1 > k0 ? k1 - k0 : 0;
-    nsplit = (keys + args.chunk - 1) / args.chunk;
-    nsplit = nsplit < 1 ? 1 : nsplit < args.splits ? nsplit : args.splits;
-    const int each = ((keys + nsplit - 1) / nsplit + 127) & ~127;
-    nsplit = each > 0 ? (keys + each - 1) / each : 1;
-    nsplit = nsplit < 1 ? 1 : nsplit;
-    if ((int)split >= nsplit) return;
-    k0 += (int)split * each;
-    k1 = k1 - k0 < each ? k1 : k0 + each;
+  int k0 = lo_any & ~31, k1 = hi_any;
+  const Cut cut = cut_of(args, k0, k1);
+  const int nsplit = cut.n;
+  if ((int)split >= nsplit) return;
+  if (nsplit > 1) {
+    k0 += (int)split * cut.each;
+    k1 = k1 - k0 < cut.each ? k1 : k0 + cut.each;
   }
 
+  // the walk: the next tile's bytes are in flight while one is computed (the
+  // first tile's while the queries are made ready), and the table entries of
+  // the one after
   Walk<D, NQ> w;
-  w.start(a, args.group, (int)kvh, 0, count, r, g, [&](int row) { return at_.row0 + row; }, bounds,
-          at_.begin);
-
-  // the walk: the next tile's bytes are in flight while one is computed, and
-  // the table entries of the one after
-  {
-    constexpr int STEP = 128;
-    const int t0 = k0 + 32 * __builtin_amdgcn_readfirstlane(wave);
-    if (t0 < k1) {
-      const Reader rd = {c, a.block_table + at_.b * a.table_width, (at_.len - 1) >> args.shift, args.shift,
-                         (int)kvh, r, g};
-      Raw<D> cur, nxt;
-      Pages p = rd.pages(t0);
-      rd.load(t0, p, cur);
-      p = rd.pages(t0 + STEP < k1 ? t0 + STEP : t0);
-      for (int t = t0; t < k1; t += STEP) {
-        const int tn = t + STEP < k1 ? t + STEP : t;
-        rd.load(tn, p, nxt);
-        p = rd.pages(tn + STEP < k1 ? tn + STEP : tn);
+  typename Walk<D, NQ>::RawQ rq;
+  constexpr int STEP = 128, S = SLOTS;
+  const int t0 = k0 + 32 * __builtin_amdgcn_readfirstlane(wave);
+  const bool any = t0 < k1;
+  const Reader rd = {c, a.block_table + (int64_t)at_.b * a.table_width, any ? (at_.len - 1) >> args.shift : 0,
+                     args.shift, (int)kvh, r, g};
+  const auto at = [&](int i) {  // i tiles ahead, the last one again past the end
+    const int t = t0 + i * STEP;
+    return t < k1 ? t : t0 + (k1 - 1 - t0) / STEP * STEP;
+  };
+  Raw<D> raw[S];
+  Pages p = {-1, -1};
+  if (any) {
+    p = rd.pages(t0);
+#pragma unroll
+    for (int u = 0; u < S - 1; ++u) {
+      const Pages pn = rd.pages(at(u + 1));
+      if (u == 0) w.load_queries(args, at_, (int)kvh, 0, r, g, rq);
+      rd.load(at(u), p, raw[u]);
+      p = pn;
+    }
+    w.start(args, (int)kvh, rq);
+    for (int i = 0; t0 + i * STEP < k1; i += S) {
+#pragma unroll
+      for (int u = 0; u < S; ++u) {
+        const int t = t0 + (i + u) * STEP;
+        if (u > 0 && t >= k1) break;
+        const Pages pn = rd.pages(at(i + u + S));
+        rd.load(at(i + u + S - 1), p, raw[(u + S - 1) % S]);
+        p = pn;
+        Raw<D>& cur = raw[u];
         const bool whole = t >= lo_all && t + 32 <= hi_all && __all(cur.ok);
         w.tile(cur, t, g, lo_any, hi_any, !whole);
-        cur = nxt;
       }
     }
+  } else {
+    w.none();
   }
 #pragma unroll
   for (int n = 0; n < NQ; ++n) w.l[n] = sum_over_g(w.l[n]);
 
   const float av = outer_alpha(c.v_amax[kvh], c.global_fp8_max);
-  const auto out_row = [&](int row) {  // token * q_heads + head
-    int64_t head;
-    const int64_t token = split_row(at_.row0 + row, args.group, head);
-    return (at_.begin + token) * a.q_heads + (int64_t)kvh * args.group + head;
-  };
   {
     // join the four wavefronts: their maxima and sums, then 64 columns at a time
     __shared__ __align__(16) float slab[4 * RW * kSlabStride];
     __shared__ float ms[4][RW], ls[4][RW];
-    __shared__ bool last;
     if (g == 0) {
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
@@ -584,11 +624,7 @@ kv_attention_keys_kernel(AttnArgs args) {
       }
     }
     __syncthreads();
-    const size_t row_floats = D + 2;
-    const uint64_t group_at = (uint64_t)tile * (uint32_t)c.kv_heads + kvh;
-    float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + NVFP4_KV_ATTENTION_COUNTER_BYTES) +
-                   group_at * args.splits * RW * row_floats;
-    float* mine = parts + (size_t)split * RW * row_floats;
+    const Parts parts = parts_of<D, RW>(args, tile, kvh);
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
       const int row = 16 * n + r;
@@ -630,78 +666,71 @@ kv_attention_keys_kernel(AttnArgs args) {
         if (nsplit == 1) {
           const bool empty = M == -__builtin_inff() && L == 0.0f;
           const float inv = empty ? 0.0f : av / L;
-          const int64_t at = out_row(row);
+          const int64_t at = out_row(args, at_, (int)kvh, row);
           uint2 y = make_uint2(bf16_pair(x.x * inv, x.y * inv), bf16_pair(x.z * inv, x.w * inv));
           if (empty) y = make_uint2(0, 0);
           *reinterpret_cast<uint2*>(a.out + at * D + 64 * j + col) = y;
           if (a.lse && j == 0 && col == 0) a.lse[at] = empty ? -__builtin_inff() : (M + __builtin_log2f(L)) / kLog2e;
         } else {
-          float* dst = mine + (size_t)row * row_floats;
-          put2(dst + 64 * j + col, x.x, x.y);
-          put2(dst + 64 * j + col + 2, x.z, x.w);
-          if (j == 0 && col == 0) put2(dst + D, M, L);
+          const int at = (int)split * RW + row;
+          *reinterpret_cast<float4*>(parts.o + (size_t)at * D + 64 * j + col) = x;
+          if (j == 0 && col == 0) parts.ml[at] = make_float2(M, L);
         }
-      }
-    }
-    if (nsplit == 1) return;
-    // arrive once the partial result has reached the level that all see
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    uint32_t* counter = static_cast<uint32_t*>(a.workspace) + group_at;
-    if (threadIdx.x == 0) {
-      last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)nsplit - 1;
-      if (last) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    __syncthreads();
-    if (!last) return;
-    // the last workgroup joins the splits in order: weights first (in the
-    // slab: at most 128 splits x 16 rows per pass), then the columns
-    float* wt = slab;  // [16 rows][kMaxSplits]
-#pragma unroll 1
-    for (int n = 0; n < NQ; ++n) {
-      const int row = 16 * n + (threadIdx.x >> 4), sub = threadIdx.x & 15;
-      const bool on = row < count;
-      const float* src = parts + (size_t)(on ? row : 0) * row_floats;
-      const size_t next = RW * row_floats;
-      float M = -__builtin_inff();
-      for (int s = sub; s < nsplit; s += 16) M = __builtin_fmaxf(M, get2(src + s * next + D).x);
-      M = __builtin_fmaxf(M, __uint_as_float(xor1_u32(u32(M))));
-      M = __builtin_fmaxf(M, __uint_as_float(xor2_u32(u32(M))));
-      M = __builtin_fmaxf(M, __uint_as_float(xor4_u32(u32(M))));
-      M = __builtin_fmaxf(M, __uint_as_float(xor8_u32(u32(M))));
-      float L = 0.0f;
-      __syncthreads();
-      for (int s = sub; s < nsplit; s += 16) {
-        const float2 ml = get2(src + s * next + D);
-        const float f = join_weight(ml.x, M);
-        wt[(threadIdx.x >> 4) * kMaxSplits + s] = f;
-        L += f * ml.y;
-      }
-      L += __uint_as_float(xor1_u32(u32(L)));
-      L += __uint_as_float(xor2_u32(u32(L)));
-      L += __uint_as_float(xor4_u32(u32(L)));
-      L += __uint_as_float(xor8_u32(u32(L)));
-      __syncthreads();
-      if (!on) continue;
-      const bool empty = M == -__builtin_inff() && L == 0.0f;
-      const float inv = empty ? 0.0f : av / L;
-      const int64_t at = out_row(row);
-      if (a.lse && sub == 0) a.lse[at] = empty ? -__builtin_inff() : (M + __builtin_log2f(L)) / kLog2e;
-      const float* f = wt + (threadIdx.x >> 4) * kMaxSplits;
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        float4 x = make_float4(0, 0, 0, 0);
-#pragma unroll 4
-        for (int s = 0; s < nsplit; ++s) {
-          const float2 y = get2(src + s * next + 64 * j + col), z = get2(src + s * next + 64 * j + col + 2);
-          x.x += f[s] * y.x; x.y += f[s] * y.y; x.z += f[s] * z.x; x.w += f[s] * z.y;
-        }
-        uint2 y = make_uint2(bf16_pair(x.x * inv, x.y * inv), bf16_pair(x.z * inv, x.w * inv));
-        if (empty) y = make_uint2(0, 0);
-        *reinterpret_cast<uint2*>(a.out + at * D + 64 * j + col) = y;
       }
     }
   }
+}
+
+// Joins the pieces of split tiles, in order: a wavefront per row, its lanes
+// first over the pieces (weights, in LDS), then over the columns.  A launch of
+// its own: joined by the last workgroup of a tile to arrive instead, the
+// pieces of one tile pass through one CU (3 x 4 drafted tokens, 32 rows x 128
+// pieces: 257 us against 61).
+template <int D, int RW>
+__global__ void __launch_bounds__(kAttnThreads) kv_attention_join_kernel(AttnArgs args) {
+  __shared__ float weight[4][kMaxSplits];
+  const nvfp4_kv_attention_args& a = args.a;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  constexpr uint32_t PER = RW / 4;  // workgroups a tile
+  const uint32_t kvh = blockIdx.x / PER % (uint32_t)a.cache.kv_heads;
+  const uint32_t tile = blockIdx.x / PER / (uint32_t)a.cache.kv_heads;
+  const int row = (int)(blockIdx.x % PER) * 4 + wave;
+  const Place at_ = place_of(args, tile, lane);
+  if (row >= at_.count) return;
+  int lo_any, hi_any, other;
+  bounds_of(args, at_, at_.row0, lo_any, other);
+  bounds_of(args, at_, at_.row0 + at_.count - 1, other, hi_any);
+  const int n = cut_of(args, lo_any & ~31, hi_any).n;
+  if (n == 1) return;  // its workgroup has written the result
+  const Parts parts = parts_of<D, RW>(args, tile, kvh);
+  const float2 none = make_float2(-__builtin_inff(), 0.0f);
+  static_assert(kMaxSplits == 128, "two pieces a lane");
+  const float2 x0 = lane < n ? parts.ml[lane * RW + row] : none;
+  const float2 x1 = lane + 64 < n ? parts.ml[(lane + 64) * RW + row] : none;
+  float M = __builtin_fmaxf(x0.x, x1.x);
+  for (int d = 1; d < 64; d <<= 1) M = __builtin_fmaxf(M, __shfl_xor(M, d));
+  const float f0 = join_weight(x0.x, M), f1 = join_weight(x1.x, M);
+  float L = f0 * x0.y + f1 * x1.y;
+  for (int d = 1; d < 64; d <<= 1) L += __shfl_xor(L, d);
+  weight[wave][lane] = f0;
+  weight[wave][lane + 64] = f1;
+  __builtin_amdgcn_wave_barrier();  // one wavefront's LDS accesses stay in order
+  constexpr int C = D / 64;  // columns C lane .. of a lane
+  float o[C] = {};
+  const float* src = parts.o + (size_t)row * D + C * lane;
+#pragma unroll 8
+  for (int s = 0; s < n; ++s) {
+    const float f = weight[wave][s];
+#pragma unroll
+    for (int i = 0; i < C; ++i) o[i] = __builtin_fmaf(f, src[(size_t)s * (RW * D) + i], o[i]);
+  }
+  const bool empty = M == -__builtin_inff() && L == 0.0f;
+  const float inv = empty ? 0.0f : outer_alpha(a.cache.v_amax[kvh], a.cache.global_fp8_max) / L;
+  const int64_t at = out_row(args, at_, (int)kvh, row);
+  uint16_t* dst = a.out + at * D + C * lane;
+#pragma unroll
+  for (int i = 0; i < C; ++i) dst[i] = empty ? (uint16_t)0 : (uint16_t)bf16_pair(o[i] * inv, 0.0f);
+  if (a.lse && lane == 0) a.lse[at] = empty ? -__builtin_inff() : (M + __builtin_log2f(L)) / kLog2e;
 }
 
 // ---------------------------------------------------------------- many rows
@@ -734,22 +763,24 @@ kv_attention_rows_kernel(AttnArgs args) {
   if (at_.count == 0) return;
   const int count = at_.count, first = wave * RW;
   const bool mine = first < count;  // the wavefront has rows
-  const auto bounds = [&](int64_t row, int& lo, int& hi) { at_.bounds(a, args.group, row, lo, hi); };
-  // bounds ascend with the row: the workgroup's keys, and the wavefront's
+  // the workgroup's keys, and the wavefront's
   int lo_wg, hi_wg, lo_wg_all, hi_wg_all, lo_any, hi_any, lo_all, hi_all;
-  bounds(at_.row0, lo_wg, hi_wg_all);
-  bounds(at_.row0 + count - 1, lo_wg_all, hi_wg);
-  bounds(at_.row0 + (mine ? first : 0), lo_any, hi_all);
-  bounds(at_.row0 + (mine && first + RW < count ? first + RW : count) - 1, lo_all, hi_any);
+  bounds_of(args, at_, at_.row0, lo_wg, hi_wg_all);
+  bounds_of(args, at_, at_.row0 + count - 1, lo_wg_all, hi_wg);
+  bounds_of(args, at_, at_.row0 + (mine ? first : 0), lo_any, hi_all);
+  bounds_of(args, at_, at_.row0 + (mine && first + RW < count ? first + RW : count) - 1, lo_all, hi_any);
 
   Walk<D, NQ> w;
-  w.start(a, args.group, (int)kvh, mine ? first : 0, count, r, g, [&](int row) { return at_.row0 + row; },
-          bounds, at_.begin);
+  {
+    typename Walk<D, NQ>::RawQ rq;
+    w.load_queries(args, at_, (int)kvh, mine ? first : 0, r, g, rq);
+    w.start(args, (int)kvh, rq);
+  }
 
   const int k0 = lo_wg & ~(BLOCK - 1), k1 = hi_wg;
   if (k0 < k1) {
-    const Reader rd = {c, a.block_table + at_.b * a.table_width, (at_.len - 1) >> args.shift, args.shift,
-                       (int)kvh, r, g};
+    const Reader rd = {c, a.block_table + (int64_t)at_.b * a.table_width, (at_.len - 1) >> args.shift,
+                       args.shift, (int)kvh, r, g};
     const int half = wave >> 1, sub = wave & 1;  // the wavefront's 32 keys of a block; t of its keys, h of its values
     // a block's quarter: NCH key pieces of 16 keys, NJ x 2 value columns of 32
     struct Quarter {
@@ -795,15 +826,17 @@ kv_attention_rows_kernel(AttnArgs args) {
     };
     Quarter x;
     Pages p = rd.pages(k0 + 32 * half);
+    const Pages p1 = rd.pages((k0 + BLOCK < k1 ? k0 + BLOCK : k0) + 32 * half);
     load(k0, p, x);
-    p = rd.pages((k0 + BLOCK < k1 ? k0 + BLOCK : k0) + 32 * half);
+    p = p1;
     put(x, k0, 0);
     lds_sync();
     int buf = 0;
     for (int t = k0; t < k1; t += BLOCK, buf ^= 1) {
       const int tn = t + BLOCK < k1 ? t + BLOCK : t;
+      const Pages pn = rd.pages((tn + BLOCK < k1 ? tn + BLOCK : tn) + 32 * half);
       load(tn, p, x);
-      p = rd.pages((tn + BLOCK < k1 ? tn + BLOCK : tn) + 32 * half);
+      p = pn;
       if (mine && t < hi_any && t + BLOCK > lo_any) {
         const int flag = __builtin_amdgcn_readfirstlane(flags[buf][0] | flags[buf][1] | flags[buf][2] | flags[buf][3]);
 #pragma unroll
@@ -861,9 +894,7 @@ kv_attention_rows_kernel(AttnArgs args) {
     if (row >= count) continue;
     const bool empty = w.m[n] == -__builtin_inff() && l == 0.0f;
     const float inv = empty ? 0.0f : av / l;
-    int64_t head;
-    const int64_t token = split_row(at_.row0 + row, args.group, head);
-    const int64_t at = (at_.begin + token) * a.q_heads + (int64_t)kvh * args.group + head;
+    const int64_t at = out_row(args, at_, (int)kvh, row);
     if (a.lse && g == 0) a.lse[at] = empty ? -__builtin_inff() : (w.m[n] + __builtin_log2f(l)) / kLog2e;
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
@@ -887,7 +918,7 @@ static AttnPlan plan_of(const nvfp4_kv_attention_args& a) {
   // rows of an average request decide the form; every form is right for all
   const int64_t batch = a.batch > 0 ? a.batch : 1;
   const int64_t rows = a.cu_q ? (a.tokens * group + batch - 1) / batch : group;
-  const int nq_most = D <= 128 ? 4 : 2;  // registers: NQ * D accumulator values a lane / 16
+  const int nq_most = keys_nq_most(D);
   p.rows_split = rows >= 128;
   p.nq = p.rows_split ? rows_nq(D) : rows <= 16 ? 1 : rows <= 32 ? 2 : nq_most;
   p.rows = 16 * p.nq * (p.rows_split ? 4 : 1);
@@ -898,21 +929,29 @@ static AttnPlan plan_of(const nvfp4_kv_attention_args& a) {
   if (a.window > 0 && a.window + p.rows / group + 64 < keys) keys = a.window + p.rows / group + 64;
   p.splits = 1;
   p.chunk = 0x7FFFFF80;
-  if (!p.rows_split && groups <= kMaxGroups && keys > 128) {
-    // keys a workgroup takes: halved from 4096 until four workgroups for each
-    // compute unit have work at the bound, 128 (one tile a wavefront) at least
-    const int64_t want = 4 * (int64_t)device_cu_count();
-    int64_t chunk = 4096;
-    while (chunk > 128 && groups * ((keys + chunk - 1) / chunk) < want) chunk /= 2;
-    int64_t splits = (keys + chunk - 1) / chunk;
-    if (splits > kMaxSplits) splits = kMaxSplits;
-    p.splits = (int)splits;
-    p.chunk = (int)chunk;
+  if (!p.rows_split && keys > 128) {
+    // Pieces a tile's keys are cut into: the least of a small model of the
+    // launch, in microseconds -- rounds of resident workgroups, each with its
+    // start and end (C0) and its keys at the speed of a loaded card (V per
+    // workgroup), and the second launch -- over full requests and over
+    // requests of 0.6 of the bound.  Measured at 64 requests of 1024 to 8192
+    // keys and 8 heads: 2 pieces 92.8 us, 4 pieces 84.8; 16 requests of up to
+    // 2000: 8 pieces 19.7, 4 pieces 16.4.
+    const double C0 = 5, V = 60.0 * 128 / D, resident = (double)device_cu_count() * attn_waves(D, p.nq);
+    const auto rounds = [&](double n) { return ceil(n / resident); };
+    double best = 0;
+    for (int n = 1; n <= kMaxSplits && (n - 1) * (int64_t)128 < keys; ++n) {
+      const double piece = C0 + (double)keys / n / V, all = (double)groups * n;
+      const double cost = (rounds(all) + rounds(0.6 * all)) * piece + (n > 1 ? 6 + 0.1 * n : 0);
+      if (n == 1 || cost < best) {
+        best = cost;
+        p.splits = n;
+      }
+    }
+    p.chunk = (int)((keys + p.splits - 1) / p.splits);
   }
   p.grid = groups * p.splits;
-  p.bytes = p.splits > 1 ? NVFP4_KV_ATTENTION_COUNTER_BYTES +
-                               (size_t)groups * p.splits * 16 * p.nq * (D + 2) * sizeof(float)
-                         : 0;
+  p.bytes = p.splits > 1 ? (size_t)groups * p.splits * p.rows * (D + 2) * sizeof(float) : 0;
   return p;
 }
 
@@ -920,17 +959,22 @@ size_t kv_attention_workspace(const nvfp4_kv_attention_args& a) { return plan_of
 
 template <int D>
 static void launch_dim(const AttnArgs& x, const AttnPlan& p, hipStream_t s) {
-  constexpr int MOST = D <= 128 ? 4 : 2;
+  constexpr int MOST = keys_nq_most(D);
   const dim3 grid((unsigned)p.grid), block(kAttnThreads);
   if (p.rows_split) hipLaunchKernelGGL((kv_attention_rows_kernel<D, rows_nq(D)>), grid, block, 0, s, x);
   else if (p.nq == 1) hipLaunchKernelGGL((kv_attention_keys_kernel<D, 1>), grid, block, 0, s, x);
   else if (p.nq == 2) hipLaunchKernelGGL((kv_attention_keys_kernel<D, 2>), grid, block, 0, s, x);
   else hipLaunchKernelGGL((kv_attention_keys_kernel<D, MOST>), grid, block, 0, s, x);
+  if (p.splits == 1) return;
+  const dim3 rows((unsigned)(p.tiles * x.a.cache.kv_heads * (p.rows / 4)));
+  if (p.nq == 1) hipLaunchKernelGGL((kv_attention_join_kernel<D, 16>), rows, block, 0, s, x);
+  else if (p.nq == 2) hipLaunchKernelGGL((kv_attention_join_kernel<D, 32>), rows, block, 0, s, x);
+  else hipLaunchKernelGGL((kv_attention_join_kernel<D, 16 * MOST>), rows, block, 0, s, x);
 }
 
 hipError_t launch_kv_attention(const nvfp4_kv_attention_args& a, hipStream_t s) {
   const AttnPlan p = plan_of(a);
-  if (p.grid > INT32_MAX) return hipErrorInvalidValue;
+  if (p.grid > INT32_MAX || p.tiles * a.cache.kv_heads * (p.rows / 4) > INT32_MAX) return hipErrorInvalidValue;
   AttnArgs x = {};
   x.a = a;
   x.rows = p.rows;

@@ -359,7 +359,7 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
     width); scale: default D^-1/2; window: attend the last `window` tokens only
     (0: all).  Returns out [tokens, q_heads, D] bf16, or (out, lse) with
     want_lse.  workspace: a uint8 tensor of at least the size the library asks
-    for, zero-filled before its first use."""
+    for."""
     t, h, d, st = _heads(q, "q", None, None, cache.head_dim, granule=8)
     _need(seq_lens, torch.int32, "seq_lens")
     batch = seq_lens.numel()
@@ -392,7 +392,7 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
         if workspace.numel() < n:
             raise ValueError(f"workspace must hold {n} bytes, got {workspace.numel()}")
     else:
-        workspace = _cached_workspace(_ATTENTION_WORKSPACES, dev, n, N.KV_ATTENTION_COUNTER_BYTES)
+        workspace = _cached_workspace(_ATTENTION_WORKSPACES, dev, n, 0)
     args.workspace = _ptr(workspace)
     _invoke("nvfp4_kv_attention", (ctypes.byref(args),), dev,
             (q, cache, block_table, seq_lens, cu_q, out, lse, workspace, args))

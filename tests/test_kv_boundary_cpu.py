@@ -209,7 +209,7 @@ def test_struct_layouts_match_the_header(tmp_path, c_name, struct):
     src = tmp_path / "layout.c"
     lines = ["#include <stddef.h>", "#include <stdio.h>", '#include "nvfp4.h"', "int main(void) {"]
     lines += [f'  printf("%zu\\n", offsetof({c_name}, {f}));' for f, _ in struct._fields_]
-    lines += [f'  printf("%zu\\n%d\\n", sizeof({c_name}), NVFP4_KV_ATTENTION_COUNTER_BYTES);',
+    lines += [f'  printf("%zu\\n", sizeof({c_name}));',
               "  return 0;", "}"]
     src.write_text("\n".join(lines) + "\n")
     exe = tmp_path / "layout"
@@ -219,8 +219,7 @@ def test_struct_layouts_match_the_header(tmp_path, c_name, struct):
         pytest.skip(f"cannot build a host program against the HIP headers: {r.stderr[:200]}")
     got = [int(v) for v in subprocess.run([str(exe)], capture_output=True, text=True,
                                           check=True).stdout.split()]
-    assert got == [getattr(struct, f).offset for f, _ in struct._fields_] + [
-        ctypes.sizeof(struct), N.KV_ATTENTION_COUNTER_BYTES]
+    assert got == [getattr(struct, f).offset for f, _ in struct._fields_] + [ctypes.sizeof(struct)]
 
 
 def test_binding_rejects_host_tensors():
