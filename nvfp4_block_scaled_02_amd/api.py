@@ -46,7 +46,10 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+    """The raw current stream of a device (without building a Stream object,
+    which costs a few microseconds a call)."""
+    i = device.index
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if i is None else i)
 
 
 def _need(t: torch.Tensor, dtype, name, numel: Optional[int] = None):

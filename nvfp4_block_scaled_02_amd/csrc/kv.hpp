@@ -2,6 +2,8 @@
 // they share.
 #pragma once
 
+#include <type_traits>
+
 #include "../../include/nvfp4.h"
 #include "common.hpp"
 #include "device.hpp"
@@ -17,8 +19,20 @@ size_t qk_norm_rope_bwd_workspace(int head_dim);
 hipError_t launch_kv_append(const nvfp4_kv_append_args& a, hipStream_t s);
 hipError_t launch_kv_read(const nvfp4_kv_cache& c, const int64_t* slots, int64_t tokens,
                           uint16_t* k_out, uint16_t* v_out, hipStream_t s);
-size_t kv_attention_workspace(const nvfp4_kv_attention_args& a);
-hipError_t launch_kv_attention(const nvfp4_kv_attention_args& a, hipStream_t s);
+// Launch shape of an attention call, from its sizes alone.
+struct AttnPlan {
+  int nq;           // 16-row tiles of a wavefront
+  bool rows_split;  // wavefronts take rows of their own (else every fourth key tile)
+  int rows;         // rows of a workgroup
+  int splits;       // most workgroups over one tile's keys
+  int chunk;        // keys a workgroup is meant to take
+  int64_t tiles;    // row tiles over all requests, at most
+  int64_t grid;
+  size_t bytes;     // of workspace
+};
+
+AttnPlan kv_attention_plan(const nvfp4_kv_attention_args& a);
+hipError_t launch_kv_attention(const nvfp4_kv_attention_args& a, const AttnPlan& p, hipStream_t s);
 
 // Byte offsets of one token's codes and scales of a head.  page < 2^31,
 // heads <= 2^10, page_size <= 2^10 and D/2 <= 2^7: the products stay below

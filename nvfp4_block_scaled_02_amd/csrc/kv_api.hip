@@ -175,7 +175,7 @@ static int attention_ok(const nvfp4_kv_attention_args& a) {
 
 size_t nvfp4_kv_attention_workspace_bytes(const nvfp4_kv_attention_args* args) {
   if (!args || attention_ok(*args) != NVFP4_OK) return 0;
-  return kv_attention_workspace(*args);
+  return kv_attention_plan(*args).bytes;
 }
 
 int nvfp4_kv_attention(const nvfp4_kv_attention_args* args, hipStream_t stream) {
@@ -189,8 +189,9 @@ int nvfp4_kv_attention(const nvfp4_kv_attention_args* args, hipStream_t stream) 
     return NVFP4_ERR_INVALID;
   if (st != NVFP4_OK) return st;
   if (a.tokens == 0) return NVFP4_OK;
-  if (kv_attention_workspace(a) != 0 && !a.workspace) return NVFP4_ERR_INVALID;
-  return status_of(launch_kv_attention(a, stream));
+  const AttnPlan plan = kv_attention_plan(a);
+  if (plan.bytes != 0 && !a.workspace) return NVFP4_ERR_INVALID;
+  return status_of(launch_kv_attention(a, plan, stream));
 }
 
 }  // extern "C"

@@ -43,17 +43,6 @@ constexpr int kMaxSplits = 128;
 constexpr int kSlabStride = 68;  // floats of a 64-column slab row: 4 apart in the banks
 constexpr float kLog2e = 1.44269504088896340736f;
 
-struct AttnPlan {
-  int nq;           // 16-row tiles of a wavefront
-  bool rows_split;  // wavefronts take rows of their own (else every fourth key tile)
-  int rows;         // rows of a workgroup
-  int splits;       // most workgroups over one tile's keys
-  int chunk;        // keys a workgroup is meant to take
-  int64_t tiles;    // row tiles over all requests, at most
-  int64_t grid;
-  size_t bytes;     // of workspace
-};
-
 struct AttnArgs {
   nvfp4_kv_attention_args a;
   int rows, splits, chunk, shift, group;
@@ -529,10 +518,10 @@ constexpr int attn_waves(int D, int NQ) {
   return D * NQ <= 64 ? 4 : D * NQ <= 128 ? 3 : D * NQ <= 256 ? 2 : 1;
 }
 
-// Most 16-row tiles of a wavefront of the kernel below.  Four of D = 128 spill
-// and leave one wavefront a SIMD: 64 rows of 8 requests over up to 8192 keys
+// Most 16-row tiles of a wavefront of the kernel below.  Four of D = 128 (two
+// of 256) spill and leave one wavefront a SIMD: 64 rows of 8 requests over up to 8192 keys
 // take 97 us that way and 44 us as two tiles of 32.
-constexpr int keys_nq_most(int D) { return D == 64 ? 4 : 2; }
+constexpr int keys_nq_most(int D) { return D == 64 ? 4 : D <= 192 ? 2 : 1; }
 
 // Few rows: the wavefronts of a workgroup take every fourth key tile.
 template <int D, int NQ>
@@ -912,7 +901,7 @@ kv_attention_rows_kernel(AttnArgs args) {
 }
 
 // ---------------------------------------------------------------- host
-static AttnPlan plan_of(const nvfp4_kv_attention_args& a) {
+AttnPlan kv_attention_plan(const nvfp4_kv_attention_args& a) {
   AttnPlan p = {};
   const int D = a.cache.head_dim, group = a.q_heads / a.cache.kv_heads;
   // rows of an average request decide the form; every form is right for all
@@ -920,7 +909,8 @@ static AttnPlan plan_of(const nvfp4_kv_attention_args& a) {
   const int64_t rows = a.cu_q ? (a.tokens * group + batch - 1) / batch : group;
   const int nq_most = keys_nq_most(D);
   p.rows_split = rows >= 128;
-  p.nq = p.rows_split ? rows_nq(D) : rows <= 16 ? 1 : rows <= 32 ? 2 : nq_most;
+  p.nq = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  p.nq = p.rows_split ? rows_nq(D) : p.nq < nq_most ? p.nq : nq_most;
   p.rows = 16 * p.nq * (p.rows_split ? 4 : 1);
   p.tiles = a.cu_q ? a.tokens * group / p.rows + a.batch + 1
                    : a.batch * ((group + p.rows - 1) / p.rows);
@@ -940,7 +930,7 @@ static AttnPlan plan_of(const nvfp4_kv_attention_args& a) {
     const double C0 = 5, V = 60.0 * 128 / D, resident = (double)device_cu_count() * attn_waves(D, p.nq);
     const auto rounds = [&](double n) { return ceil(n / resident); };
     double best = 0;
-    for (int n = 1; n <= kMaxSplits && (n - 1) * (int64_t)128 < keys; ++n) {
+    for (int n = 1; n <= kMaxSplits && (n - 1) * (int64_t)128 < keys; n += 1 + n / 16) {
       const double piece = C0 + (double)keys / n / V, all = (double)groups * n;
       const double cost = (rounds(all) + rounds(0.6 * all)) * piece + (n > 1 ? 6 + 0.1 * n : 0);
       if (n == 1 || cost < best) {
@@ -955,25 +945,30 @@ static AttnPlan plan_of(const nvfp4_kv_attention_args& a) {
   return p;
 }
 
-size_t kv_attention_workspace(const nvfp4_kv_attention_args& a) { return plan_of(a).bytes; }
-
 template <int D>
 static void launch_dim(const AttnArgs& x, const AttnPlan& p, hipStream_t s) {
   constexpr int MOST = keys_nq_most(D);
   const dim3 grid((unsigned)p.grid), block(kAttnThreads);
-  if (p.rows_split) hipLaunchKernelGGL((kv_attention_rows_kernel<D, rows_nq(D)>), grid, block, 0, s, x);
-  else if (p.nq == 1) hipLaunchKernelGGL((kv_attention_keys_kernel<D, 1>), grid, block, 0, s, x);
-  else if (p.nq == 2) hipLaunchKernelGGL((kv_attention_keys_kernel<D, 2>), grid, block, 0, s, x);
-  else hipLaunchKernelGGL((kv_attention_keys_kernel<D, MOST>), grid, block, 0, s, x);
-  if (p.splits == 1) return;
+  if (p.rows_split) {
+    hipLaunchKernelGGL((kv_attention_rows_kernel<D, rows_nq(D)>), grid, block, 0, s, x);
+    return;
+  }
   const dim3 rows((unsigned)(p.tiles * x.a.cache.kv_heads * (p.rows / 4)));
-  if (p.nq == 1) hipLaunchKernelGGL((kv_attention_join_kernel<D, 16>), rows, block, 0, s, x);
-  else if (p.nq == 2) hipLaunchKernelGGL((kv_attention_join_kernel<D, 32>), rows, block, 0, s, x);
-  else hipLaunchKernelGGL((kv_attention_join_kernel<D, 16 * MOST>), rows, block, 0, s, x);
+  const auto launch = [&](auto nq) {
+    constexpr int NQ = decltype(nq)::value;
+    hipLaunchKernelGGL((kv_attention_keys_kernel<D, NQ>), grid, block, 0, s, x);
+    if (p.splits > 1) hipLaunchKernelGGL((kv_attention_join_kernel<D, 16 * NQ>), rows, block, 0, s, x);
+  };
+  if (p.nq == 1) launch(std::integral_constant<int, 1>{});
+  if constexpr (MOST >= 2) {
+    if (p.nq == 2) launch(std::integral_constant<int, 2>{});
+  }
+  if constexpr (MOST >= 4) {
+    if (p.nq == 4) launch(std::integral_constant<int, 4>{});
+  }
 }
 
-hipError_t launch_kv_attention(const nvfp4_kv_attention_args& a, hipStream_t s) {
-  const AttnPlan p = plan_of(a);
+hipError_t launch_kv_attention(const nvfp4_kv_attention_args& a, const AttnPlan& p, hipStream_t s) {
   if (p.grid > INT32_MAX || p.tiles * a.cache.kv_heads * (p.rows / 4) > INT32_MAX) return hipErrorInvalidValue;
   AttnArgs x = {};
   x.a = a;

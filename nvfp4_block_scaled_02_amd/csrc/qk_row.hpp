@@ -4,8 +4,6 @@
 // cache's write and read (kv_cache.hip).
 #pragma once
 
-#include <type_traits>
-
 #include "kv.hpp"
 
 namespace nvfp4 {

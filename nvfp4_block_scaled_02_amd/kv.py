@@ -16,7 +16,7 @@ from typing import Optional
 import torch
 
 from . import _native as N
-from .api import _invoke, _need, _ptr, _SELECT, _stream, default_global_max
+from .api import _invoke, _need, _SELECT, _stream, default_global_max
 
 _PAIRS = {"halves": N.PAIRS_HALVES, "neighbours": N.PAIRS_NEIGHBOURS}
 
@@ -27,15 +27,30 @@ def _choice(table, value, name):
     return table[value]
 
 
-def _heads(x: torch.Tensor, name, tokens=None, heads=None, dim=None, granule=4):
+_BF16, _F32, _I32, _I64, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
+
+
+def _ptr(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _check(t, dtype, name, numel=None):
+    """_need, with its answer first where nothing is wrong (these calls are
+    made every token: the checks' own time counts)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous()
+            and (numel is None or t.numel() == numel)):
+        _need(t, dtype, name, numel)
+
+
+def _heads(x, name, tokens=None, heads=None, dim=None, granule=4):
     """[tokens, heads, D] bf16 on a GPU with dense heads: (tokens, heads, D,
     elements from token to token)."""
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if x.device.type != "cuda":
+    if not x.is_cuda:
         raise ValueError(f"{name} must live on a GPU device, got {x.device}")
-    if x.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {x.dtype}")
+    if x.dtype is not _BF16:
+        raise TypeError(f"{name} must be {_BF16}, got {x.dtype}")
     if x.dim() != 3:
         raise ValueError(f"{name} must be 3-D [tokens, heads, head_dim]")
     t, h, d = x.shape
@@ -133,32 +148,32 @@ def kv_plan(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.T
     width] (int32).  free_pages [num_pages] and free_count [1] (int32) are the
     stack of free pages; the result's free_count is the count after the step.
     tokens: at least the sum of new_lens (the rest is padding)."""
-    _need(ctx_lens, torch.int32, "ctx_lens")
+    _check(ctx_lens, _I32, "ctx_lens")
     batch = ctx_lens.numel()
-    _need(new_lens, torch.int32, "new_lens", batch)
-    _need(block_table, torch.int32, "block_table")
+    _check(new_lens, _I32, "new_lens", batch)
+    _check(block_table, _I32, "block_table")
     if block_table.dim() != 2 or block_table.shape[0] != batch:
         raise ValueError(f"block_table must be [{batch}, width], got {tuple(block_table.shape)}")
-    _need(free_pages, torch.int32, "free_pages", num_pages)
-    _need(free_count, torch.int32, "free_count", 1)
+    _check(free_pages, _I32, "free_pages", num_pages)
+    _check(free_count, _I32, "free_count", 1)
     dev = ctx_lens.device
     if out is None:
-        e = lambda n, t=torch.int32: torch.empty(n, dtype=t, device=dev)  # noqa: E731
-        out = KVPlan(e(batch + 1), e(batch), e(tokens), e(tokens, torch.int64), e(1), e(1))
+        # one allocation: the 32-bit outputs one after another
+        words = torch.empty(2 * batch + tokens + 3, dtype=_I32, device=dev)
+        cu, lens, pos, count, refused = words.split((batch + 1, batch, tokens, 1, 1))
+        out = KVPlan(cu, lens, pos, torch.empty(tokens, dtype=_I64, device=dev), count, refused)
     else:
-        _need(out.cu_new, torch.int32, "cu_new", batch + 1)
-        _need(out.seq_lens, torch.int32, "seq_lens", batch)
-        _need(out.positions, torch.int32, "positions", tokens)
-        _need(out.slots, torch.int64, "slots", tokens)
-        _need(out.free_count, torch.int32, "free_count", 1)
-        _need(out.refused, torch.int32, "refused", 1)
+        _check(out.cu_new, _I32, "cu_new", batch + 1)
+        _check(out.seq_lens, _I32, "seq_lens", batch)
+        _check(out.positions, _I32, "positions", tokens)
+        _check(out.slots, _I64, "slots", tokens)
+        _check(out.free_count, _I32, "free_count", 1)
+        _check(out.refused, _I32, "refused", 1)
     args = N.KVPlanArgs(
-        ctx_lens=_ptr(ctx_lens), new_lens=_ptr(new_lens), batch=batch,
-        block_table=_ptr(block_table), table_width=block_table.shape[1],
-        free_pages=_ptr(free_pages), free_count=_ptr(free_count), num_pages=num_pages,
-        page_size=page_size, tokens=tokens, cu_new=_ptr(out.cu_new), seq_lens=_ptr(out.seq_lens),
-        positions=_ptr(out.positions), slots=_ptr(out.slots), free_count_out=_ptr(out.free_count),
-        refused=_ptr(out.refused))
+        ctx_lens.data_ptr(), new_lens.data_ptr(), batch, block_table.data_ptr(),
+        block_table.shape[1], free_pages.data_ptr(), free_count.data_ptr(), num_pages, page_size,
+        tokens, out.cu_new.data_ptr(), out.seq_lens.data_ptr(), out.positions.data_ptr(),
+        out.slots.data_ptr(), out.free_count.data_ptr(), out.refused.data_ptr())
     _invoke("nvfp4_kv_plan", (ctypes.byref(args),), dev,
             (ctx_lens, new_lens, block_table, free_pages, free_count, out, args))
     return out
@@ -173,53 +188,53 @@ def rope_table(positions: int, rot_dim: int, *, base: float = 10000.0, device="c
     return a.cos().float().contiguous(), a.sin().float().contiguous()
 
 
-def _qk(q, k, positions, cos, sin, q_weight, k_weight, eps, pairs):
-    """nvfp4_qk_args without outputs; q or k may be None."""
-    first = q if q is not None else k
-    if first is None:
-        raise ValueError("pass q, k or both")
-    a = N.QKArgs(eps=eps, pairs=_choice(_PAIRS, pairs, "pairs"))
-    t = d = None
-    for x, w, n in ((q, q_weight, "q"), (k, k_weight, "k")):
-        if x is None:
-            if w is not None:
-                raise ValueError(f"{n}_weight without {n}")
-            continue
-        t, h, d, st = _heads(x, n, t, None, d)
-        setattr(a, n, x.data_ptr())
-        setattr(a, n + "_heads", h)
-        setattr(a, n + "_stride", st)
+def _side(x, w, n, t, d):
+    """(pointer, tokens, heads, D, stride, weight pointer) of queries or keys."""
+    if x is None:
         if w is not None:
-            _need(w, torch.bfloat16, n + "_weight", d)
-            setattr(a, n + "_weight", w.data_ptr())
-    a.tokens, a.head_dim = t, d
-    if cos is None or sin is None or positions is None:
-        if not (cos is None and sin is None and positions is None):
-            raise ValueError("pass positions, cos and sin, or none of them")
-    else:
-        _need(cos, torch.float32, "cos")
+            raise ValueError(f"{n}_weight without {n}")
+        return 0, t, 0, d, 0, 0
+    t, h, d, st = _heads(x, n, t, None, d)
+    if w is not None:
+        _check(w, _BF16, n + "_weight", d)
+        return x.data_ptr(), t, h, d, st, w.data_ptr()
+    return x.data_ptr(), t, h, d, st, 0
+
+
+def _out_of(x, given, n):
+    """Output of side n like x, given or new and dense: (tensor, pointer, stride)."""
+    if x is None:
+        return None, 0, 0
+    if given is None:
+        given = torch.empty(x.shape, dtype=_BF16, device=x.device)
+        return given, given.data_ptr(), x.shape[1] * x.shape[2]
+    return given, given.data_ptr(), _heads(given, n + "_out", *x.shape)[3]
+
+
+def _qk(q, k, positions, cos, sin, q_weight, k_weight, eps, pairs, q_out, k_out, want_k=True):
+    """nvfp4_qk_args and its outputs; q or k may be None."""
+    if q is None and k is None:
+        raise ValueError("pass q, k or both")
+    pr = _choice(_PAIRS, pairs, "pairs")
+    qp, t, hq, d, qs, qw = _side(q, q_weight, "q", None, None)
+    kp, t, hk, d, ks, kw = _side(k, k_weight, "k", t, d)
+    pp = cp = sp = top = rot = 0
+    if cos is not None and sin is not None and positions is not None:
+        _check(cos, _F32, "cos")
         if cos.dim() != 2 or cos.shape[1] * 2 > d:
             raise ValueError(f"cos must be [positions, rot_dim / 2] with rot_dim <= {d}, "
                              f"got {tuple(cos.shape)}")
-        _need(sin, torch.float32, "sin", cos.numel())
-        _need(positions, torch.int32, "positions", t)
-        a.positions, a.cos, a.sin = positions.data_ptr(), cos.data_ptr(), sin.data_ptr()
-        a.max_pos, a.rot_dim = cos.shape[0], 2 * cos.shape[1]
-    return a
-
-
-def _qk_out(a, x, given, n):
-    """Output of side n like x: given, or new and dense."""
-    if x is None:
-        return None
-    if given is None:
-        given = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
-        st = x.shape[1] * x.shape[2]
-    else:
-        st = _heads(given, n + "_out", *x.shape)[3]
-    setattr(a, n + "_out", given.data_ptr())
-    setattr(a, n + "_out_stride", st)
-    return given
+        _check(sin, _F32, "sin", cos.numel())
+        _check(positions, _I32, "positions", t)
+        pp, cp, sp = positions.data_ptr(), cos.data_ptr(), sin.data_ptr()
+        top, rot = cos.shape
+        rot *= 2
+    elif not (cos is None and sin is None and positions is None):
+        raise ValueError("pass positions, cos and sin, or none of them")
+    qo, qop, qos = _out_of(q, q_out, "q")
+    ko, kop, kos = _out_of(k, k_out, "k") if want_k else (None, 0, 0)
+    return N.QKArgs(qp, kp, t, hq, hk, d, qs, ks, pp, cp, sp, top, rot, pr, qw, kw, eps, qop, kop,
+                    qos, kos), qo, ko
 
 
 def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor] = None,
@@ -231,9 +246,8 @@ def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor] = None,
     weight [D]) and rotation of its first 2 * cos.shape[1] values by the
     angles of positions [tokens] (int32): (q_out, k_out).  out: (q_out,
     k_out), which may be q and k."""
-    a = _qk(q, k, positions, cos, sin, q_weight, k_weight, eps, pairs)
     qo, ko = out if out is not None else (None, None)
-    qo, ko = _qk_out(a, q, qo, "q"), _qk_out(a, k, ko, "k")
+    a, qo, ko = _qk(q, k, positions, cos, sin, q_weight, k_weight, eps, pairs, qo, ko)
     _invoke("nvfp4_qk_norm_rope", (ctypes.byref(a),), (q if q is not None else k).device,
             (q, k, positions, cos, sin, q_weight, k_weight, qo, ko, a))
     return qo, ko
@@ -273,21 +287,22 @@ def qk_norm_rope_bwd(dq_out: Optional[torch.Tensor], dk_out: Optional[torch.Tens
     """Gradient of qk_norm_rope at (q, k) for the gradients dq_out and dk_out
     of its results: (dq, dk, dq_weight, dk_weight), the last two float32 [D]
     or None.  out: optional {"dq", "dk", "dq_weight", "dk_weight"}."""
-    a = _qk(q, k, positions, cos, sin, q_weight, k_weight, eps, pairs)
-    out = dict(out or {})
+    out = out or {}
+    a, dq, dk = _qk(q, k, positions, cos, sin, q_weight, k_weight, eps, pairs, out.get("dq"),
+                    out.get("dk"))
     dev = (q if q is not None else k).device
-    grads, strides, dws = [], [], []
+    strides, dws = [], []
     for n, x, g, w in (("q", q, dq_out, q_weight), ("k", k, dk_out, k_weight)):
         if (x is None) != (g is None):
             raise ValueError(f"pass {n} and d{n}_out, or neither")
         strides.append(_heads(g, f"d{n}_out", *x.shape)[3] if g is not None else 0)
-        grads.append(_qk_out(a, x, out.get("d" + n), n))
         dw = None
         if w is not None:
             dw = out.get(f"d{n}_weight")
             if dw is None:
-                dw = torch.empty(a.head_dim, dtype=torch.float32, device=dev)
-            _need(dw, torch.float32, f"d{n}_weight", a.head_dim)
+                dw = torch.empty(a.head_dim, dtype=_F32, device=dev)
+            else:
+                _check(dw, _F32, f"d{n}_weight", a.head_dim)
         dws.append(dw)
     ws = None
     if q_weight is not None or k_weight is not None:
@@ -300,8 +315,8 @@ def qk_norm_rope_bwd(dq_out: Optional[torch.Tensor], dk_out: Optional[torch.Tens
     _invoke("nvfp4_qk_norm_rope_bwd",
             (ctypes.byref(a), _ptr(dq_out), strides[0], _ptr(dk_out), strides[1], _ptr(dws[0]),
              _ptr(dws[1]), _ptr(ws)), dev,
-            (q, k, positions, cos, sin, q_weight, k_weight, dq_out, dk_out, grads, dws, ws, a))
-    return grads[0], grads[1], dws[0], dws[1]
+            (q, k, positions, cos, sin, q_weight, k_weight, dq_out, dk_out, dq, dk, dws, ws, a))
+    return dq, dk, dws[0], dws[1]
 
 
 # ---------------------------------------------------------------- write and read
@@ -315,13 +330,14 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Ten
     [tokens, kv_heads, D] into the cache at slots [tokens] (int64; a slot
     outside the cache is skipped), and returns q after its norm and rotation
     (None without q).  select: "6" or "4over6"."""
-    a = _qk(q, k, positions, cos, sin, q_weight, k_weight, eps, pairs)
-    t, st = a.tokens, _heads(v, "v", a.tokens, cache.kv_heads, cache.head_dim)[3]
-    _heads(k, "k", t, cache.kv_heads, cache.head_dim)
-    _need(slots, torch.int64, "slots", t)
-    qo = _qk_out(a, q, q_out, "q")
-    args = N.KVAppendArgs(qk=a, v=v.data_ptr(), v_stride=st, slots=slots.data_ptr(),
-                          cache=cache._args, select=_choice(_SELECT, select, "select"))
+    a, qo, _ = _qk(q, k, positions, cos, sin, q_weight, k_weight, eps, pairs, q_out, None, False)
+    t = a.tokens
+    if a.k_heads != cache.kv_heads or a.head_dim != cache.head_dim:
+        raise ValueError(f"k must be [tokens, {cache.kv_heads}, {cache.head_dim}], got {tuple(k.shape)}")
+    st = _heads(v, "v", t, cache.kv_heads, cache.head_dim)[3]
+    _check(slots, _I64, "slots", t)
+    args = N.KVAppendArgs(a, v.data_ptr(), st, slots.data_ptr(), cache._args,
+                          _choice(_SELECT, select, "select"))
     _invoke("nvfp4_kv_append", (ctypes.byref(args),), k.device,
             (cache, q, k, v, slots, positions, cos, sin, q_weight, k_weight, qo, args))
     return qo
@@ -330,13 +346,15 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Ten
 def kv_read(cache: KVCache, slots: torch.Tensor, *, out: Optional[tuple] = None):
     """(k, v) bf16 [tokens, kv_heads, D]: what the cache holds at slots
     (int64); 0 for a slot outside the cache."""
-    _need(slots, torch.int64, "slots")
+    _check(slots, _I64, "slots")
     n = slots.numel()
-    shape = (n, cache.kv_heads, cache.head_dim)
+    h, d = cache.kv_heads, cache.head_dim
     if out is None:
-        out = tuple(torch.empty(shape, dtype=torch.bfloat16, device=slots.device) for _ in "kv")
-    for o, name in zip(out, ("k_out", "v_out")):
-        _need(o, torch.bfloat16, name, n * shape[1] * shape[2])
+        out = (torch.empty((n, h, d), dtype=_BF16, device=slots.device),
+               torch.empty((n, h, d), dtype=_BF16, device=slots.device))
+    else:
+        for o, name in zip(out, ("k_out", "v_out")):
+            _check(o, _BF16, name, n * h * d)
     _invoke("nvfp4_kv_read", (ctypes.byref(cache._args), _ptr(slots), n, _ptr(out[0]), _ptr(out[1])),
             slots.device, (cache, slots, out))
     return out
@@ -360,35 +378,35 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
     (0: all).  Returns out [tokens, q_heads, D] bf16, or (out, lse) with
     want_lse.  workspace: a uint8 tensor of at least the size the library asks
     for."""
-    t, h, d, st = _heads(q, "q", None, None, cache.head_dim, granule=8)
-    _need(seq_lens, torch.int32, "seq_lens")
+    t, h, d, st = _heads(q, "q", None, None, cache.head_dim, 8)
+    _check(seq_lens, _I32, "seq_lens")
     batch = seq_lens.numel()
-    _need(block_table, torch.int32, "block_table")
+    _check(block_table, _I32, "block_table")
     if block_table.dim() != 2 or block_table.shape[0] != batch:
         raise ValueError(f"block_table must be [{batch}, width], got {tuple(block_table.shape)}")
     if cu_q is not None:
-        _need(cu_q, torch.int32, "cu_q", batch + 1)
+        _check(cu_q, _I32, "cu_q", batch + 1)
     elif t != batch:
         raise ValueError(f"without cu_q every request has one query: {t} rows, {batch} requests")
     dev = q.device
     if out is None:
-        out = torch.empty((t, h, d), dtype=torch.bfloat16, device=dev)
+        out = torch.empty((t, h, d), dtype=_BF16, device=dev)
     else:
-        _need(out, torch.bfloat16, "out", t * h * d)
+        _check(out, _BF16, "out", t * h * d)
     if lse is None and want_lse:
-        lse = torch.empty((t, h), dtype=torch.float32, device=dev)
+        lse = torch.empty((t, h), dtype=_F32, device=dev)
     elif lse is not None:
-        _need(lse, torch.float32, "lse", t * h)
+        _check(lse, _F32, "lse", t * h)
     width = block_table.shape[1]
-    args = N.KVAttentionArgs(
-        q=q.data_ptr(), tokens=t, q_stride=st, q_heads=h, cache=cache._args,
-        block_table=_ptr(block_table), batch=batch, table_width=width, seq_lens=_ptr(seq_lens),
-        cu_q=_ptr(cu_q), max_seq_len=width * cache.page_size if max_seq_len is None else max_seq_len,
-        scale=d ** -0.5 if scale is None else scale, causal=int(causal), window=window,
-        out=_ptr(out), lse=_ptr(lse))
+    if max_seq_len is None:
+        max_seq_len = width * cache.page_size
+    args = N.KVAttentionArgs(q.data_ptr(), t, st, h, cache._args, block_table.data_ptr(), batch,
+                             width, seq_lens.data_ptr(), _ptr(cu_q), max_seq_len,
+                             d ** -0.5 if scale is None else scale, int(causal), window,
+                             out.data_ptr(), _ptr(lse), 0)
     n = N.lib().nvfp4_kv_attention_workspace_bytes(ctypes.byref(args))
     if workspace is not None:
-        _need(workspace, torch.uint8, "workspace")
+        _check(workspace, _U8, "workspace")
         if workspace.numel() < n:
             raise ValueError(f"workspace must hold {n} bytes, got {workspace.numel()}")
     else:
