@@ -77,71 +77,66 @@ __device__ __forceinline__ void quad_quantize(const float (&x)[8], const TensorS
 template <int LPH, int PAIRS, int SELECT>
 __global__ void __launch_bounds__(kRowThreads)
 kv_append_kernel(nvfp4_kv_append_args p, RowGrid grid) {
-  constexpr int N = 64 / LPH;
   const nvfp4_qk_args& a = p.qk;
   const nvfp4_kv_cache& c = p.cache;
-  const int D = a.head_dim, sub = (int)(threadIdx.x & 63) / LPH;
+  const int D = a.head_dim, heads = a.k_heads;
   const RowMap<LPH> m(D, a.rot_dim, PAIRS);
   const Row8 wq = weight_load(a.q_weight, m), wk = weight_load(a.k_weight, m);
-  const double inv_d = 1.0 / D;
+  const double inv_d = 1.0 / D, eps = a.eps;
   const int64_t slots_end = c.num_pages * c.page_size;
   const int shift = __builtin_ctz((unsigned)c.page_size);
-  const int kfirst = grid.q_groups, vfirst = grid.q_groups + grid.k_groups;
   for (int64_t wave = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
        wave < grid.waves; wave += (int64_t)gridDim.x * 4) {
     const RowTask t = row_task(wave, grid);
     const int64_t slot = p.slots[t.token];
     const bool stored = slot >= 0 && slot < slots_end;
     const RowAngles ang = row_angles(a, m, t.token);
-    const auto head_of = [&](int g) { return (g < kfirst ? g : g < vfirst ? g - kfirst : g - vfirst) * N + sub; };
-    const auto on = [&](int g) { return head_of(g) < (g < kfirst ? a.q_heads : a.k_heads); };
-    const auto load = [&](int g) {
-      return row_load((g < kfirst ? a.q + t.token * a.q_stride : g < vfirst ? a.k + t.token * a.k_stride
-                                                                            : p.v + t.token * p.v_stride) +
-                          head_of(g) * D, m, on(g));
+    const RowPart pq = part_of(t, 0, grid.q_groups);
+    row_walk(a.q + t.token * a.q_stride, a.q_heads, D, pq.g0, pq.g1, m, [&](int h, const Row8& v) {
+      const Row8 y = row_norm_rope<LPH, PAIRS>(v, m, a.q_weight != nullptr, wq, eps, inv_d, ang);
+      if (m.active && h < a.q_heads) row_store(a.q_out + t.token * a.q_out_stride + h * D, m, y);
+    });
+    if (!stored) continue;  // the wavefront together
+    // quantizes a head's values under its outer amax and hands over the bytes
+    const auto quantize = [&](int h, const Row8& v, const float* amax, const auto& write) {
+      float x[8];
+      v.unpack(x);
+      const int hc = h < heads ? h : heads - 1;
+      uint32_t codes[2], scale[2];
+      quad_quantize<SELECT>(x, tensor_scale(amax[hc], c.global_fp8_max), codes, scale);
+      if (m.active && h < heads)
+        write(KvAddr{(slot >> shift) * heads + h, (int)(slot & (c.page_size - 1)), c.page_size, D}, codes, scale);
     };
-    Row8 in = load(t.first);
-    for (int g = t.first; g < t.last; ++g) {
-      const Row8 next = load(g + 1 < t.last ? g + 1 : g);
-      const int h = head_of(g);
-      const bool isq = g < kfirst, isv = g >= vfirst;
-      if (!isv) {
-        in = row_norm_rope<LPH, PAIRS>(in, m, (isq ? a.q_weight : a.k_weight) != nullptr, isq ? wq : wk,
-                                       a.eps, inv_d, ang);
-        if (isq) row_store(a.q_out + t.token * a.q_out_stride + h * D, m, in, on(g));
-      }
-      if (!isq && stored) {  // the wavefront together
-        float x[8];
-        in.unpack(x);
-        const int hc = h < c.kv_heads ? h : 0;
-        const TensorScale ts = tensor_scale((isv ? c.v_amax : c.k_amax)[hc], c.global_fp8_max);
-        uint32_t codes[2], scale[2];
-        quad_quantize<SELECT>(x, ts, codes, scale);
-        const KvAddr k = {(slot >> shift) * c.kv_heads + hc, (int)(slot & (c.page_size - 1)), c.page_size, D};
-        if (m.active && on(g) && !isv) {
-          uint8_t* kc = c.k_codes + k.k_code();
-          *reinterpret_cast<uint16_t*>(kc + m.e0 / 2) = (uint16_t)codes[0];
-          *reinterpret_cast<uint16_t*>(kc + m.e1 / 2) = (uint16_t)codes[1];
-          if ((threadIdx.x & 3) == 0) {
-            uint8_t* ks = c.k_scales + k.k_scale();
-            ks[m.e0 / 16] = (uint8_t)scale[0];
-            ks[m.e1 / 16] = (uint8_t)scale[1];
-          }
-        } else if (m.active && on(g)) {
-          uint8_t* vc = c.v_codes + k.v_code();
-          vc[8 * (m.e0 / 2)] = (uint8_t)codes[0];
-          vc[8 * (m.e0 / 2 + 1)] = (uint8_t)(codes[0] >> 8);
-          vc[8 * (m.e1 / 2)] = (uint8_t)codes[1];
-          vc[8 * (m.e1 / 2 + 1)] = (uint8_t)(codes[1] >> 8);
-          if ((threadIdx.x & 3) == 0) {
-            uint8_t* vs = c.v_scales + k.v_scale();
-            vs[8 * (m.e0 / 16)] = (uint8_t)scale[0];
-            vs[8 * (m.e1 / 16)] = (uint8_t)scale[1];
-          }
-        }
-      }
-      in = next;
-    }
+    const RowPart pk = part_of(t, grid.q_groups, grid.k_groups);
+    row_walk(a.k + t.token * a.k_stride, heads, D, pk.g0, pk.g1, m, [&](int h, const Row8& v) {
+      quantize(h, row_norm_rope<LPH, PAIRS>(v, m, a.k_weight != nullptr, wk, eps, inv_d, ang), c.k_amax,
+               [&](const KvAddr& k, const uint32_t (&codes)[2], const uint32_t (&scale)[2]) {
+                 uint8_t* kc = c.k_codes + k.k_code();
+                 *reinterpret_cast<uint16_t*>(kc + m.e0 / 2) = (uint16_t)codes[0];
+                 *reinterpret_cast<uint16_t*>(kc + m.e1 / 2) = (uint16_t)codes[1];
+                 if ((threadIdx.x & 3) == 0) {
+                   uint8_t* ks = c.k_scales + k.k_scale();
+                   ks[m.e0 / 16] = (uint8_t)scale[0];
+                   ks[m.e1 / 16] = (uint8_t)scale[1];
+                 }
+               });
+    });
+    const RowPart pv = part_of(t, grid.q_groups + grid.k_groups, grid.v_groups);
+    row_walk(p.v + t.token * p.v_stride, heads, D, pv.g0, pv.g1, m, [&](int h, const Row8& v) {
+      quantize(h, v.or_zero(m.active), c.v_amax,
+               [&](const KvAddr& k, const uint32_t (&codes)[2], const uint32_t (&scale)[2]) {
+                 uint8_t* vc = c.v_codes + k.v_code();
+                 vc[8 * (m.e0 / 2)] = (uint8_t)codes[0];
+                 vc[8 * (m.e0 / 2 + 1)] = (uint8_t)(codes[0] >> 8);
+                 vc[8 * (m.e1 / 2)] = (uint8_t)codes[1];
+                 vc[8 * (m.e1 / 2 + 1)] = (uint8_t)(codes[1] >> 8);
+                 if ((threadIdx.x & 3) == 0) {
+                   uint8_t* vs = c.v_scales + k.v_scale();
+                   vs[8 * (m.e0 / 16)] = (uint8_t)scale[0];
+                   vs[8 * (m.e1 / 16)] = (uint8_t)scale[1];
+                 }
+               });
+    });
   }
 }
 

@@ -10,32 +10,24 @@ namespace nvfp4 {
 template <int LPH, int PAIRS>
 __global__ void __launch_bounds__(kRowThreads)
 qk_norm_rope_kernel(nvfp4_qk_args a, RowGrid grid) {
-  constexpr int N = 64 / LPH;
-  const int D = a.head_dim, sub = (int)(threadIdx.x & 63) / LPH;
+  const int D = a.head_dim;
   const RowMap<LPH> m(D, a.rot_dim, PAIRS);
   const Row8 wq = weight_load(a.q_weight, m), wk = weight_load(a.k_weight, m);
-  const double inv_d = 1.0 / D;
+  const double inv_d = 1.0 / D, eps = a.eps;
   for (int64_t wave = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
        wave < grid.waves; wave += (int64_t)gridDim.x * 4) {
     const RowTask t = row_task(wave, grid);
     const RowAngles ang = row_angles(a, m, t.token);
-    // the values of group g in each lane; queries and keys differ in three numbers
-    const auto head_of = [&](int g) { return (g < grid.q_groups ? g : g - grid.q_groups) * N + sub; };
-    const auto on = [&](int g) { return head_of(g) < (g < grid.q_groups ? a.q_heads : a.k_heads); };
-    const auto load = [&](int g) {
-      return row_load((g < grid.q_groups ? a.q + t.token * a.q_stride : a.k + t.token * a.k_stride) +
-                          head_of(g) * D, m, on(g));
+    const auto side = [&](const uint16_t* x, uint16_t* out, int heads, const RowPart& p, bool norm, const Row8& w) {
+      row_walk(x, heads, D, p.g0, p.g1, m, [&](int h, const Row8& v) {
+        const Row8 y = row_norm_rope<LPH, PAIRS>(v, m, norm, w, eps, inv_d, ang);
+        if (m.active && h < heads) row_store(out + h * D, m, y);
+      });
     };
-    Row8 x = load(t.first);
-    for (int g = t.first; g < t.last; ++g) {
-      const Row8 next = load(g + 1 < t.last ? g + 1 : g);
-      const bool isq = g < grid.q_groups;
-      const Row8 y = row_norm_rope<LPH, PAIRS>(x, m, (isq ? a.q_weight : a.k_weight) != nullptr,
-                                               isq ? wq : wk, a.eps, inv_d, ang);
-      row_store((isq ? a.q_out + t.token * a.q_out_stride : a.k_out + t.token * a.k_out_stride) +
-                    head_of(g) * D, m, y, on(g));
-      x = next;
-    }
+    side(a.q + t.token * a.q_stride, a.q_out + t.token * a.q_out_stride, a.q_heads,
+         part_of(t, 0, grid.q_groups), a.q_weight != nullptr, wq);
+    side(a.k + t.token * a.k_stride, a.k_out + t.token * a.k_out_stride, a.k_heads,
+         part_of(t, grid.q_groups, grid.k_groups), a.k_weight != nullptr, wk);
   }
 }
 
@@ -143,7 +135,7 @@ __device__ __forceinline__ double sum_slots(const double* slots, int n, int e, i
 // atomic addition, the same bits on every run.  Slots are written and read at
 // the level that the whole GPU sees, so no cache is written back.
 template <int LPH, int PAIRS>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kRowThreads, 4)
 qk_norm_rope_bwd_kernel(BwdArgs b) {
   constexpr int N = 64 / LPH;
   __shared__ double part[4][2 * 256];
@@ -152,57 +144,59 @@ qk_norm_rope_bwd_kernel(BwdArgs b) {
   const RowGrid& grid = b.grid;
   const int D = a.head_dim, sub = (int)(threadIdx.x & 63) / LPH, wv = threadIdx.x >> 6;
   const RowMap<LPH> m(D, a.rot_dim, PAIRS);
-  const Row8 wq = weight_load(a.q_weight, m), wk = weight_load(a.k_weight, m);
   const float inv_d = 1.0f / (float)D, eps = a.eps;
-  double sum_q[8] = {}, sum_k[8] = {};
-  for (int64_t wave = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(wv); wave < grid.waves;
-       wave += (int64_t)gridDim.x * 4) {
-    const RowTask t = row_task(wave, grid);
-    const RowAngles ang = row_angles(a, m, t.token);
-    // the groups of one kind (queries, then keys): their sums of dw
-    const auto side = [&](const uint16_t* x, int64_t xs, const uint16_t* y, int64_t ys, uint16_t* d, int64_t ds,
-                          int heads, int g0, int g1, bool norm, const Row8& weight, double (&sum)[8]) {
-      if (g0 >= g1) return;
-      x += t.token * xs + sub * D;
-      y += t.token * ys + sub * D;
-      d += t.token * ds + sub * D;
-      const auto on = [&](int g) { return g * N + sub < heads; };
+  const bool sums = b.dqw || b.dkw;
+  // all of the wavefront's query heads, then its key heads: one set of sums in
+  // registers at a time
+  const auto side = [&](const uint16_t* x0, int64_t xs, const uint16_t* y0, int64_t ys, uint16_t* d0, int64_t ds,
+                        int heads, int kind, const uint16_t* w, int column0) {
+    const bool norm = w != nullptr;
+    const Row8 weight = weight_load(w, m);
+    double sum[8] = {};
+    for (int64_t wave = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(wv); wave < grid.waves;
+         wave += (int64_t)gridDim.x * 4) {
+      const RowTask t = row_task(wave, grid);
+      const RowPart p = kind == 0 ? part_of(t, 0, grid.q_groups) : part_of(t, grid.q_groups, grid.k_groups);
+      if (p.g0 >= p.g1) continue;
+      const RowAngles ang = row_angles(a, m, t.token);
+      const uint16_t* x = x0 + t.token * xs;
+      const uint16_t* y = y0 + t.token * ys;
+      uint16_t* d = d0 + t.token * ds;
+      const auto head_of = [&](int g) { return g * N + sub; };
+      const auto load = [&](const uint16_t* s, int g) {
+        const int h = head_of(g);
+        return row_load(s + (h < heads ? h : heads - 1) * D, m);
+      };
       float dw[8] = {};
-      Row8 xv = row_load(x + g0 * N * D, m, on(g0)), yv = row_load(y + g0 * N * D, m, on(g0));
-      for (int g = g0; g < g1; ++g) {
-        const int gn = g + 1 < g1 ? g + 1 : g;
-        const Row8 xn = row_load(x + gn * N * D, m, on(gn)), yn = row_load(y + gn * N * D, m, on(gn));
-        row_store(d + g * N * D, m, row_bwd<LPH, PAIRS>(xv, yv, m, norm, weight, eps, inv_d, ang, dw), on(g));
+      Row8 xv = load(x, p.g0), yv = load(y, p.g0);
+      for (int g = p.g0; g < p.g1; ++g) {
+        const int gn = g + 1 < p.g1 ? g + 1 : g;
+        const Row8 xn = load(x, gn), yn = load(y, gn);
+        // lanes without values, and heads past the last one, add nothing
+        const bool on = m.active && head_of(g) < heads;
+        const Row8 r = row_bwd<LPH, PAIRS>(xv.or_zero(on), yv.or_zero(on), m, norm, weight, eps, inv_d, ang, dw);
+        if (on) row_store(d + head_of(g) * D, m, r);
         xv = xn;
         yv = yn;
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum[i] += dw[i];
-    };
-    const int q1 = t.last < grid.q_groups ? t.last : grid.q_groups;
-    const int k0 = (t.first > grid.q_groups ? t.first : grid.q_groups) - grid.q_groups;
-    side(a.q, a.q_stride, b.gq, b.gq_stride, a.q_out, a.q_out_stride, a.q_heads, t.first, q1,
-         a.q_weight != nullptr, wq, sum_q);
-    side(a.k, a.k_stride, b.gk, b.gk_stride, a.k_out, a.k_out_stride, a.k_heads, k0, t.last - grid.q_groups,
-         a.k_weight != nullptr, wk, sum_k);
-  }
-  if (!b.dqw && !b.dkw) return;
-  // the wavefront's heads, then the workgroup's wavefronts
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    for (int d = LPH; d < 64; d <<= 1) {
-      sum_q[i] += __shfl_xor(sum_q[i], d);
-      sum_k[i] += __shfl_xor(sum_k[i], d);
     }
-  if ((threadIdx.x & 63) < LPH && m.active) {
+    if (!sums) return;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      part[wv][m.e0 + i] = sum_q[i];
-      part[wv][m.e1 + i] = sum_q[4 + i];
-      part[wv][D + m.e0 + i] = sum_k[i];
-      part[wv][D + m.e1 + i] = sum_k[4 + i];
+    for (int i = 0; i < 8; ++i)
+      for (int k = LPH; k < 64; k <<= 1) sum[i] += __shfl_xor(sum[i], k);
+    if ((threadIdx.x & 63) < LPH && m.active) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        part[wv][column0 + m.e0 + i] = sum[i];
+        part[wv][column0 + m.e1 + i] = sum[4 + i];
+      }
     }
-  }
+  };
+  side(a.q, a.q_stride, b.gq, b.gq_stride, a.q_out, a.q_out_stride, a.q_heads, 0, a.q_weight, 0);
+  side(a.k, a.k_stride, b.gk, b.gk_stride, a.k_out, a.k_out_stride, a.k_heads, 1, a.k_weight, D);
+  if (!sums) return;
   __syncthreads();
   const int n = 2 * D, G = gridDim.x;
   double* slots = reinterpret_cast<double*>(b.ws + kBwdHead);

@@ -23,20 +23,15 @@ struct RowMap {
   bool active;  // the lane holds values (D / 8 need not be a power of two)
   bool rotated;
   __device__ __forceinline__ RowMap(int D, int rot, int pairs) {
-    const int u = (int)(threadIdx.x & (LPH - 1));
+    const int u = (int)(threadIdx.x & (LPH - 1)), v = u - rot / 8;
+    const bool halves = pairs == NVFP4_PAIRS_HALVES;
     active = u < D / 8;
     rotated = u < rot / 8;
-    if (rotated) {
-      e0 = 4 * u;
-      e1 = rot / 2 + 4 * u;
-      j0 = pairs == NVFP4_PAIRS_HALVES ? 4 * u : 2 * u;
-      j1 = pairs == NVFP4_PAIRS_HALVES ? 4 * u : rot / 4 + 2 * u;
-    } else {
-      const int v = u - rot / 8;
-      e0 = rot + 4 * v;
-      e1 = rot + (D - rot) / 2 + 4 * v;
-      j0 = j1 = 0;
-    }
+    // a lane without values reads value 0 and uses none of it
+    e0 = !active ? 0 : rotated ? 4 * u : rot + 4 * v;
+    e1 = !active ? 0 : rotated ? rot / 2 + 4 * u : rot + (D - rot) / 2 + 4 * v;
+    j0 = !rotated ? 0 : halves ? 4 * u : 2 * u;
+    j1 = !rotated ? 0 : halves ? 4 * u : rot / 4 + 2 * u;
   }
 };
 
@@ -47,23 +42,42 @@ struct Row8 {
     x[0] = bf16_lo(a.x); x[1] = bf16_hi(a.x); x[2] = bf16_lo(a.y); x[3] = bf16_hi(a.y);
     x[4] = bf16_lo(b.x); x[5] = bf16_hi(b.x); x[6] = bf16_lo(b.y); x[7] = bf16_hi(b.y);
   }
+  __device__ __forceinline__ Row8 or_zero(bool keep) const {
+    return Row8{make_uint2(keep ? a.x : 0u, keep ? a.y : 0u), make_uint2(keep ? b.x : 0u, keep ? b.y : 0u)};
+  }
 };
 
+// Without a branch: a load that some lanes skip makes the wait for an older
+// one wait for this one too.
 template <int LPH>
-__device__ __forceinline__ Row8 row_load(const uint16_t* p, const RowMap<LPH>& m, bool on = true) {
-  Row8 r = {make_uint2(0, 0), make_uint2(0, 0)};
-  if (m.active && on) {
-    r.a = *reinterpret_cast<const uint2*>(p + m.e0);
-    r.b = *reinterpret_cast<const uint2*>(p + m.e1);
-  }
-  return r;
+__device__ __forceinline__ Row8 row_load(const uint16_t* p, const RowMap<LPH>& m) {
+  return Row8{*reinterpret_cast<const uint2*>(p + m.e0), *reinterpret_cast<const uint2*>(p + m.e1)};
 }
 
 template <int LPH>
-__device__ __forceinline__ void row_store(uint16_t* p, const RowMap<LPH>& m, const Row8& r, bool on = true) {
-  if (m.active && on) {
-    *reinterpret_cast<uint2*>(p + m.e0) = r.a;
-    *reinterpret_cast<uint2*>(p + m.e1) = r.b;
+__device__ __forceinline__ void row_store(uint16_t* p, const RowMap<LPH>& m, const Row8& r) {
+  *reinterpret_cast<uint2*>(p + m.e0) = r.a;
+  *reinterpret_cast<uint2*>(p + m.e1) = r.b;
+}
+
+// Walks the head groups [g0, g1) of one token's heads at x: f(head, values)
+// for each, with the next group's values in flight.  Heads past the last one
+// repeat it; f is told by its head number.
+template <int LPH, class F>
+__device__ __forceinline__ void row_walk(const uint16_t* x, int heads, int D, int g0, int g1,
+                                         const RowMap<LPH>& m, const F& f) {
+  constexpr int N = 64 / LPH;
+  if (g0 >= g1) return;
+  const int sub = (int)(threadIdx.x & 63) / LPH;
+  const auto load = [&](int g) {
+    const int h = g * N + sub;
+    return row_load(x + (h < heads ? h : heads - 1) * D, m);
+  };
+  Row8 v = load(g0);
+  for (int g = g0; g < g1; ++g) {
+    const Row8 next = load(g + 1 < g1 ? g + 1 : g);
+    f(g * N + sub, v);
+    v = next;
   }
 }
 
@@ -115,8 +129,13 @@ __device__ __forceinline__ void row_rotate(R (&y)[8], const RowAngles& g) {
   for (int i = 0; i < 4; ++i) {
     const R a = y[pair_a(PAIRS, i)], b = y[pair_b(PAIRS, i)];
     const R c = (R)g.c[i], s = DIR > 0 ? (R)g.s[i] : -(R)g.s[i];
-    y[pair_a(PAIRS, i)] = a * c - b * s;
-    y[pair_b(PAIRS, i)] = b * c + a * s;
+    if constexpr (sizeof(R) == 8) {
+      y[pair_a(PAIRS, i)] = __builtin_fma(a, c, -(b * s));
+      y[pair_b(PAIRS, i)] = __builtin_fma(b, c, a * s);
+    } else {
+      y[pair_a(PAIRS, i)] = __builtin_fmaf(a, c, -(b * s));
+      y[pair_b(PAIRS, i)] = __builtin_fmaf(b, c, a * s);
+    }
   }
 }
 
@@ -165,7 +184,7 @@ __device__ __forceinline__ Row8 row_norm_rope(const Row8& in, const RowMap<LPH>&
                                               const Row8& weight, double eps, double inv_d,
                                               const RowAngles& g) {
   float x[8];
-  in.unpack(x);
+  in.or_zero(m.active).unpack(x);
   double y[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) y[i] = (double)x[i];
@@ -186,7 +205,7 @@ __device__ __forceinline__ Row8 row_norm_rope(const Row8& in, const RowMap<LPH>&
 // The lane's part of a weight; zeros without one.
 template <int LPH>
 __device__ __forceinline__ Row8 weight_load(const uint16_t* w, const RowMap<LPH>& m) {
-  return row_load(w, m, w != nullptr);
+  return w ? row_load(w, m) : Row8{make_uint2(0, 0), make_uint2(0, 0)};
 }
 
 // A wavefront takes one token and a run of its head groups (64 / LPH heads
@@ -230,6 +249,15 @@ __device__ __forceinline__ RowTask row_task(int64_t wave, const RowGrid& g) {
   const int groups = g.q_groups + g.k_groups + g.v_groups;
   const int first = part * g.per_wave, end = first + g.per_wave;
   return RowTask{g.parts == 1 ? wave : (int64_t)cut, first, end < groups ? end : groups};
+}
+
+// The part of a task's groups that lies in [from, from + n), counted from `from`.
+struct RowPart {
+  int g0, g1;
+};
+__device__ __forceinline__ RowPart part_of(const RowTask& t, int from, int n) {
+  const int a = t.first - from, b = t.last - from;
+  return RowPart{a > 0 ? a : 0, b < n ? b : n};
 }
 
 inline int lanes_per_head(int D) { return D <= 32 ? 4 : D <= 64 ? 8 : D <= 128 ? 16 : 32; }
