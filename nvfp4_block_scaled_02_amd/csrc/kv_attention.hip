@@ -17,7 +17,7 @@
 //   softmax       per lane, in the exponent of 2: the running maximum moves
 //     only when a score passes it by more than 2^8 (weights stay below 2^8,
 //     far inside binary16), so a tile usually needs no exchange between lanes
-//     and no rescaling; the sums stay per lane until the end
+//     and no rescaling; the weights' sum is one more product, with ones
 //   O^T += V^T P^T  lane (m, g) reads keys 8 g .. 8 g + 7 of 4 value columns
 //     as the cache holds them (8 tokens side by side); lane (n, g)'s weights
 //     of keys 8 g .. 8 g + 7 are already the product's other operand.
@@ -52,20 +52,13 @@ struct AttnArgs {
 // ---------------------------------------------------------------- lanes
 __device__ __forceinline__ uint32_t u32(float v) { return __float_as_uint(v); }
 
-// max / sum over the four lanes of a query (lane % 16 equal), in all of them
+// max over the four lanes of a query (lane % 16 equal), in all of them
 __device__ __forceinline__ float max_over_g(float v) {
   auto a = __builtin_amdgcn_permlane32_swap(u32(v), u32(v), false, false);
   v = __builtin_fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
   auto b = __builtin_amdgcn_permlane16_swap(u32(v), u32(v), false, false);
   return __builtin_fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
-__device__ __forceinline__ float sum_over_g(float v) {
-  auto a = __builtin_amdgcn_permlane32_swap(u32(v), u32(v), false, false);
-  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-  auto b = __builtin_amdgcn_permlane16_swap(u32(v), u32(v), false, false);
-  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
-}
-
 __device__ __forceinline__ f16x2 fp4_pair(uint32_t w, int sel) {
   switch (sel) {
     case 0: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0);
@@ -101,86 +94,6 @@ struct Raw {
 // Pages of the lane's key group and value group of a tile; -1: none.
 struct Pages {
   int k, v;
-};
-
-// One tile's worth of addresses.  The table entry of a group past the last
-// key is that of the last one (its tokens are masked).
-struct Reader {
-  const nvfp4_kv_cache& c;
-  const int32_t* table;  // of the request
-  int last;              // last table entry that may be read
-  int shift, kvh, r, g;
-  // Always a vector load (one line, all lanes): loads return in order, so it
-  // goes ahead of the tile loads it will be used after.  A scalar load where a
-  // tile lies in one page made the compiler wait for every load in flight.
-  __device__ __forceinline__ Pages pages(int tile0) const {
-    const int ik = (tile0 + 8 * (r >> 2)) >> shift, iv = (tile0 + 8 * g) >> shift;
-    return Pages{table[ik < last ? ik : last], table[iv < last ? iv : last]};
-  }
-  // Codes and scales of one 16-key product (t of the tile): D / 8 bytes and D /
-  // 64 scale bytes of the lane's key.
-  template <int D>
-  __device__ __forceinline__ void load_keys(int tile0, int t, uint32_t page, uint32_t (&k)[D / 32], uint32_t& sc) const {
-    constexpr int NCH = D / 32;
-    // tokens from the start of the cache (page < 2^31, heads and page size <= 2^10)
-    const uint64_t kt = (uint64_t)page * (uint32_t)(c.kv_heads << shift) + ((uint64_t)kvh << shift) +
-                        (((uint32_t)tile0 + 8 * (r >> 2)) & ((1u << shift) - 1)) + (r & 3) + 4 * t;
-    const uint8_t* p = c.k_codes + kt * (D / 2) + g * (D / 8);
-    const uint8_t* s = c.k_scales + kt * (D / 16) + g * (NCH / 2);
-    if constexpr (NCH % 4 == 0) {
-#pragma unroll
-      for (int i = 0; i < NCH / 4; ++i) {
-        const uint4 x = *reinterpret_cast<const uint4*>(p + 16 * i);
-        k[4 * i] = x.x; k[4 * i + 1] = x.y; k[4 * i + 2] = x.z; k[4 * i + 3] = x.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < NCH / 2; ++i) {
-        const uint2 x = *reinterpret_cast<const uint2*>(p + 8 * i);
-        k[2 * i] = x.x; k[2 * i + 1] = x.y;
-      }
-    }
-    if constexpr (NCH == 2) sc = s[0];
-    else if constexpr (NCH == 4) sc = *reinterpret_cast<const uint16_t*>(s);
-    else if constexpr (NCH == 6) sc = s[0] | (uint32_t)s[1] << 8 | (uint32_t)s[2] << 16;
-    else sc = *reinterpret_cast<const uint32_t*>(s);
-  }
-  __device__ __forceinline__ uint64_t value_tokens(int tile0, uint32_t page) const {
-    return (uint64_t)page * (uint32_t)(c.kv_heads << shift) + ((uint64_t)kvh << shift) +
-           (((uint32_t)tile0 + 8 * g) & ((1u << shift) - 1));
-  }
-  // Product t of the tile's keys, half h (one column pair of two) of its values.
-  template <int D, class Q>
-  __device__ __forceinline__ void load_quarter(int tile0, int sub, const Pages& p, Q& x) const {
-    const uint32_t n = (uint32_t)c.num_pages;
-    load_keys<D>(tile0, sub, (uint32_t)p.k < n ? (uint32_t)p.k : 0u, x.k, x.ks);
-    x.ok = (uint32_t)p.v < n;
-    const uint64_t vt = value_tokens(tile0, x.ok ? (uint32_t)p.v : 0u);
-    const uint8_t* vc = c.v_codes + vt * (D / 2) + 16 * r + 8 * sub;
-    const uint8_t* vs = c.v_scales + vt * (D / 16) + 8 * (r >> 2);
-#pragma unroll
-    for (int j = 0; j < D / 64; ++j) {
-      x.v[j] = *reinterpret_cast<const uint2*>(vc + 256 * j);
-      x.vs[j] = *reinterpret_cast<const uint2*>(vs + 32 * j);
-    }
-  }
-  template <int D>
-  __device__ __forceinline__ void load(int tile0, const Pages& p, Raw<D>& w) const {
-    constexpr int NCH = Raw<D>::NCH;
-    const uint32_t n = (uint32_t)c.num_pages;
-    const uint32_t pk = (uint32_t)p.k < n ? (uint32_t)p.k : 0u;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) load_keys<D>(tile0, t, pk, w.k[t], w.ks[t]);
-    w.ok = (uint32_t)p.v < n;
-    const uint64_t vt = value_tokens(tile0, w.ok ? (uint32_t)p.v : 0u);
-    const uint8_t* vc = c.v_codes + vt * (D / 2) + 16 * r;
-    const uint8_t* vs = c.v_scales + vt * (D / 16) + 8 * (r >> 2);
-#pragma unroll
-    for (int j = 0; j < NCH / 2; ++j) {
-      w.v[j] = *reinterpret_cast<const uint4*>(vc + 256 * j);
-      w.vs[j] = *reinterpret_cast<const uint2*>(vs + 32 * j);
-    }
-  }
 };
 
 // A byte holds two columns of one token; the products want 8 tokens of one
@@ -280,6 +193,98 @@ __device__ __forceinline__ int64_t out_row(const AttnArgs& args, const Place& at
   return (int64_t)(at.begin + (int)token) * args.a.q_heads + kvh * args.group + (int)(rr - token * (uint32_t)args.group);
 }
 
+// Where a lane reads.  The four pointers hold what does not change from tile
+// to tile (array, head, the lane's place among 32 tokens); a tile adds its
+// page and, in pages of more than 32 tokens, its place in the page: two
+// instructions a pointer.  The table entry of a group past the last key is
+// that of the last one (its tokens are masked).
+template <int D>
+struct Reader {
+  static constexpr int NCH = D / 32;
+  const uint8_t *kc, *ks, *vc, *vs;
+  const int32_t* table;  // of the request
+  int last;              // last table entry that may be read
+  int shift, r, g;
+  uint32_t pages_end, page_tokens;  // pages; tokens of a page over all heads
+  __device__ __forceinline__ Reader(const AttnArgs& args, const Place& at, int kvh, int r_, int g_) : r(r_), g(g_) {
+    const nvfp4_kv_cache& c = args.a.cache;
+    shift = args.shift;
+    table = args.a.block_table + (int64_t)at.b * args.a.table_width;
+    last = at.len > 0 ? (at.len - 1) >> shift : 0;
+    pages_end = (uint32_t)c.num_pages;
+    page_tokens = (uint32_t)c.kv_heads << shift;  // <= 2^20
+    const int mask = (1 << shift) - 1;
+    const int64_t kt = ((int64_t)kvh << shift) + ((8 * (r >> 2)) & mask) + (r & 3);
+    const int64_t vt = ((int64_t)kvh << shift) + ((8 * g) & mask);
+    kc = c.k_codes + kt * (D / 2) + g * (D / 8);
+    ks = c.k_scales + kt * (D / 16) + g * (NCH / 2);
+    vc = c.v_codes + vt * (D / 2) + 16 * r;
+    vs = c.v_scales + vt * (D / 16) + 8 * (r >> 2);
+  }
+  // Loads return in order, so these go ahead of the tile loads they will be
+  // used after; and without a branch or a scalar load for tiles in one page,
+  // either of which makes the compiler wait for all that is in flight (64
+  // requests of up to 8192 keys: 93 us so, 89 as it is).
+  __device__ __forceinline__ Pages pages(int tile0) const {
+    const int ik = (tile0 + 8 * (r >> 2)) >> shift, iv = (tile0 + 8 * g) >> shift;
+    return Pages{table[ik < last ? ik : last], table[iv < last ? iv : last]};
+  }
+  // bytes from a lane's pointer to its tokens of a tile, at `per` bytes a token
+  __device__ __forceinline__ uint64_t ahead(int tile0, uint32_t page, int per) const {
+    const uint32_t in_page = (uint32_t)tile0 & ((1u << shift) - 1) & ~31u;
+    return (uint64_t)page * (page_tokens * (uint32_t)per) + in_page * (uint32_t)per;
+  }
+  // Codes and scales of one 16-key product (t of the tile): D / 8 bytes and D /
+  // 64 scale bytes of the lane's key.
+  __device__ __forceinline__ void load_keys(int tile0, int t, uint32_t page, uint32_t (&k)[NCH], uint32_t& sc) const {
+    const uint8_t* p = kc + ahead(tile0, page, D / 2) + 4 * t * (D / 2);
+    const uint8_t* s = ks + ahead(tile0, page, D / 16) + 4 * t * (D / 16);
+    if constexpr (NCH % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < NCH / 4; ++i) {
+        const uint4 x = *reinterpret_cast<const uint4*>(p + 16 * i);
+        k[4 * i] = x.x; k[4 * i + 1] = x.y; k[4 * i + 2] = x.z; k[4 * i + 3] = x.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NCH / 2; ++i) {
+        const uint2 x = *reinterpret_cast<const uint2*>(p + 8 * i);
+        k[2 * i] = x.x; k[2 * i + 1] = x.y;
+      }
+    }
+    if constexpr (NCH == 2) sc = s[0];
+    else if constexpr (NCH == 4) sc = *reinterpret_cast<const uint16_t*>(s);
+    else if constexpr (NCH == 6) sc = s[0] | (uint32_t)s[1] << 8 | (uint32_t)s[2] << 16;
+    else sc = *reinterpret_cast<const uint32_t*>(s);
+  }
+  __device__ __forceinline__ uint32_t usable(int page) const { return (uint32_t)page < pages_end ? (uint32_t)page : 0u; }
+  // Product t of the tile's keys, half h (one column pair of two) of its values.
+  template <class Q>
+  __device__ __forceinline__ void load_quarter(int tile0, int sub, const Pages& p, Q& x) const {
+    load_keys(tile0, sub, usable(p.k), x.k, x.ks);
+    x.ok = (uint32_t)p.v < pages_end;
+    const uint8_t* c = vc + ahead(tile0, usable(p.v), D / 2) + 8 * sub;
+    const uint8_t* s = vs + ahead(tile0, usable(p.v), D / 16);
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) {
+      x.v[j] = *reinterpret_cast<const uint2*>(c + 256 * j);
+      x.vs[j] = *reinterpret_cast<const uint2*>(s + 32 * j);
+    }
+  }
+  __device__ __forceinline__ void load(int tile0, const Pages& p, Raw<D>& w) const {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) load_keys(tile0, t, usable(p.k), w.k[t], w.ks[t]);
+    w.ok = (uint32_t)p.v < pages_end;
+    const uint8_t* c = vc + ahead(tile0, usable(p.v), D / 2);
+    const uint8_t* s = vs + ahead(tile0, usable(p.v), D / 16);
+#pragma unroll
+    for (int j = 0; j < NCH / 2; ++j) {
+      w.v[j] = *reinterpret_cast<const uint4*>(c + 256 * j);
+      w.vs[j] = *reinterpret_cast<const uint2*>(s + 32 * j);
+    }
+  }
+};
+
 // ---------------------------------------------------------------- one tile
 template <int D, int NQ>
 struct Walk {
@@ -287,7 +292,8 @@ struct Walk {
   f16x8 q[NQ][NCH];
   f32x4 o[NQ][NJ][4];  // [j][e][i]: query n, column 64 j + 16 g + 4 i + e
   float factor[NQ];    // binary32 factor of a row's scores
-  float m[NQ], thr[NQ], l[NQ];
+  float m[NQ], thr[NQ];
+  f32x4 l[NQ];         // sum of a row's weights, four times
   int lo[NQ], hi[NQ];  // keys that the row attends
 
   // partial: some row does not attend some key of the tile.
@@ -354,16 +360,14 @@ struct Walk {
         for (int e = 0; e < 4; ++e) o[n][j][e] *= keep;
     }
     const float base = m[n] == -__builtin_inff() ? 0.0f : -m[n];
-    float t[8], sum = 0.0f;
+    f16x8 p, ones;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      t[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(i < 4 ? s0[i % 4] : s1[i % 4], factor[n], base));
-      sum += t[i];
+      p[i] = (_Float16)__builtin_amdgcn_exp2f(__builtin_fmaf(i < 4 ? s0[i % 4] : s1[i % 4], factor[n], base));
+      ones[i] = (_Float16)1.0f;
     }
-    l[n] += sum;
-    f16x8 p;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = (_Float16)t[i];
+    // the sum over the tile's keys, of the weights as they are used
+    l[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, p, l[n], 0, 0, 0);
     return p;
   }
 
@@ -420,7 +424,7 @@ struct Walk {
       // a score of -inf stays below every other one
       factor[n] = factor[n] == 0.0f ? 0x1p-126f : factor[n];
       m[n] = thr[n] = -__builtin_inff();
-      l[n] = 0.0f;
+      l[n] = f32x4{0, 0, 0, 0};
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
 #pragma unroll
@@ -433,7 +437,7 @@ struct Walk {
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
       m[n] = -__builtin_inff();
-      l[n] = 0.0f;
+      l[n] = f32x4{0, 0, 0, 0};
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
 #pragma unroll
@@ -515,9 +519,15 @@ __device__ __forceinline__ float join_weight(float m, float M) {
 // Wavefronts of a SIMD that the registers are shared out for: as many as fit
 // without spilling (512 registers a lane at one wavefront).
 constexpr int attn_waves(int D, int NQ) {
+#ifdef W1
+  if (D * NQ == 128) return W1;
+#endif
   return D * NQ <= 64 ? 4 : D * NQ <= 128 ? 3 : D * NQ <= 256 ? 2 : 1;
 }
 
+#ifndef SL
+#define SL 2
+#endif
 // Most 16-row tiles of a wavefront of the kernel below.  Four of D = 128 (two
 // of 256) spill and leave one wavefront a SIMD: 64 rows of 8 requests over up to 8192 keys
 // take 97 us that way and 44 us as two tiles of 32.
@@ -527,7 +537,7 @@ constexpr int keys_nq_most(int D) { return D == 64 ? 4 : D <= 192 ? 2 : 1; }
 template <int D, int NQ>
 __global__ void __launch_bounds__(kAttnThreads, attn_waves(D, NQ))
 kv_attention_keys_kernel(AttnArgs args) {
-  constexpr int NJ = D / 64, RW = 16 * NQ, SLOTS = 2;
+  constexpr int NJ = D / 64, RW = 16 * NQ, SLOTS = SL;
   const nvfp4_kv_attention_args& a = args.a;
   const nvfp4_kv_cache& c = a.cache;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
@@ -563,8 +573,7 @@ kv_attention_keys_kernel(AttnArgs args) {
   constexpr int STEP = 128, S = SLOTS;
   const int t0 = k0 + 32 * __builtin_amdgcn_readfirstlane(wave);
   const bool any = t0 < k1;
-  const Reader rd = {c, a.block_table + (int64_t)at_.b * a.table_width, any ? (at_.len - 1) >> args.shift : 0,
-                     args.shift, (int)kvh, r, g};
+  const Reader<D> rd(args, at_, (int)kvh, r, g);
   const auto at = [&](int i) {  // i tiles ahead, the last one again past the end
     const int t = t0 + i * STEP;
     return t < k1 ? t : t0 + (k1 - 1 - t0) / STEP * STEP;
@@ -597,9 +606,6 @@ kv_attention_keys_kernel(AttnArgs args) {
   } else {
     w.none();
   }
-#pragma unroll
-  for (int n = 0; n < NQ; ++n) w.l[n] = sum_over_g(w.l[n]);
-
   const float av = outer_alpha(c.v_amax[kvh], c.global_fp8_max);
   {
     // join the four wavefronts: their maxima and sums, then 64 columns at a time
@@ -609,7 +615,7 @@ kv_attention_keys_kernel(AttnArgs args) {
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
         ms[wave][16 * n + r] = w.m[n];
-        ls[wave][16 * n + r] = w.l[n];
+        ls[wave][16 * n + r] = w.l[n][0];
       }
     }
     __syncthreads();
@@ -768,8 +774,7 @@ kv_attention_rows_kernel(AttnArgs args) {
 
   const int k0 = lo_wg & ~(BLOCK - 1), k1 = hi_wg;
   if (k0 < k1) {
-    const Reader rd = {c, a.block_table + (int64_t)at_.b * a.table_width, (at_.len - 1) >> args.shift,
-                       args.shift, (int)kvh, r, g};
+    const Reader<D> rd(args, at_, (int)kvh, r, g);
     const int half = wave >> 1, sub = wave & 1;  // the wavefront's 32 keys of a block; t of its keys, h of its values
     // a block's quarter: NCH key pieces of 16 keys, NJ x 2 value columns of 32
     struct Quarter {
@@ -777,7 +782,7 @@ kv_attention_rows_kernel(AttnArgs args) {
       uint2 v[NJ], vs[NJ];
       bool ok;
     };
-    const auto load = [&](int t0, const Pages& p, Quarter& x) { rd.template load_quarter<D>(t0 + 32 * half, sub, p, x); };
+    const auto load = [&](int t0, const Pages& p, Quarter& x) { rd.load_quarter(t0 + 32 * half, sub, p, x); };
     const auto put = [&](Quarter& x, int t0, int buf) {
       const f16x2 s01 = fp8_lo(x.ks), s23 = fp8_hi(x.ks);
 #pragma unroll
@@ -878,7 +883,7 @@ kv_attention_rows_kernel(AttnArgs args) {
   const float av = outer_alpha(c.v_amax[kvh], c.global_fp8_max);
 #pragma unroll
   for (int n = 0; n < NQ; ++n) {
-    const float l = sum_over_g(w.l[n]);
+    const float l = w.l[n][0];
     const int row = first + 16 * n + r;
     if (row >= count) continue;
     const bool empty = w.m[n] == -__builtin_inff() && l == 0.0f;
