@@ -519,15 +519,9 @@ __device__ __forceinline__ float join_weight(float m, float M) {
 // Wavefronts of a SIMD that the registers are shared out for: as many as fit
 // without spilling (512 registers a lane at one wavefront).
 constexpr int attn_waves(int D, int NQ) {
-#ifdef W1
-  if (D * NQ == 128) return W1;
-#endif
   return D * NQ <= 64 ? 4 : D * NQ <= 128 ? 3 : D * NQ <= 256 ? 2 : 1;
 }
 
-#ifndef SL
-#define SL 2
-#endif
 // Most 16-row tiles of a wavefront of the kernel below.  Four of D = 128 (two
 // of 256) spill and leave one wavefront a SIMD: 64 rows of 8 requests over up to 8192 keys
 // take 97 us that way and 44 us as two tiles of 32.
@@ -537,7 +531,7 @@ constexpr int keys_nq_most(int D) { return D == 64 ? 4 : D <= 192 ? 2 : 1; }
 template <int D, int NQ>
 __global__ void __launch_bounds__(kAttnThreads, attn_waves(D, NQ))
 kv_attention_keys_kernel(AttnArgs args) {
-  constexpr int NJ = D / 64, RW = 16 * NQ, SLOTS = SL;
+  constexpr int NJ = D / 64, RW = 16 * NQ, SLOTS = 2;
   const nvfp4_kv_attention_args& a = args.a;
   const nvfp4_kv_cache& c = a.cache;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
@@ -676,20 +670,40 @@ kv_attention_keys_kernel(AttnArgs args) {
   }
 }
 
-// Joins the pieces of split tiles, in order: a wavefront per row, its lanes
-// first over the pieces (weights, in LDS), then over the columns.  A launch of
-// its own: joined by the last workgroup of a tile to arrive instead, the
-// pieces of one tile pass through one CU (3 x 4 drafted tokens, 32 rows x 128
-// pieces: 257 us against 61).
-template <int D, int RW>
-__global__ void __launch_bounds__(kAttnThreads) kv_attention_join_kernel(AttnArgs args) {
-  __shared__ float weight[4][kMaxSplits];
+// Joins the pieces of split tiles, in order: a wavefront per row, or, of many
+// pieces, a workgroup per row, each wavefront taking every fourth piece (16 of
+// them and more: one token over 8191 13.6 -> 11.9 us, 3 x 4 drafted tokens over
+// up to 131072 99 -> 90; 8 x 8 over up to 8192, few pieces, 40 against 52 the
+// other way).  A launch of its own: joined by the last workgroup of a tile to
+// arrive instead, the pieces of one tile pass through one CU (32 rows x 128
+// pieces: 257 us in all against 119).  What a piece holds is asked for before
+// it is known how many there are (the workspace has room for the most), so one
+// memory latency covers both.
+constexpr int kManyPieces = 16;
+template <int D, int RW, int WAVES>
+__global__ void __launch_bounds__(kAttnThreads) kv_attention_join_kernel(AttnArgs args, int rows) {
+  __shared__ float part[WAVES == 1 ? 1 : WAVES][D];
   const nvfp4_kv_attention_args& a = args.a;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  constexpr uint32_t PER = RW / 4;  // workgroups a tile
-  const uint32_t kvh = blockIdx.x / PER % (uint32_t)a.cache.kv_heads;
-  const uint32_t tile = blockIdx.x / PER / (uint32_t)a.cache.kv_heads;
-  const int row = (int)(blockIdx.x % PER) * 4 + wave;
+  constexpr int ROWS = 4 / WAVES;  // of a workgroup
+  const int first = WAVES == 1 ? 0 : wave;
+  const uint32_t per = (uint32_t)(rows + ROWS - 1) / ROWS;  // workgroups a tile
+  const uint32_t rest = blockIdx.x / per, tile = rest / (uint32_t)a.cache.kv_heads;
+  const uint32_t kvh = rest - tile * (uint32_t)a.cache.kv_heads;
+  const int row = (int)(blockIdx.x - rest * per) * ROWS + (WAVES == 1 ? wave : 0);
+  if (row >= rows) return;
+  const Parts parts = parts_of<D, RW>(args, tile, kvh);
+  constexpr int C = D / 64, AHEAD = 4;  // columns C lane .. of a lane; pieces asked for ahead
+  const float2* ml = parts.ml + row;
+  const float* src = parts.o + (size_t)row * D + C * lane;
+  const auto piece = [&](int i) { return (size_t)(i < args.splits ? i : args.splits - 1); };
+  static_assert(kMaxSplits == 128, "two pieces a lane");
+  float2 x0 = ml[piece(lane) * RW], x1 = ml[piece(lane + 64) * RW];
+  float ahead[AHEAD][C];
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+    for (int k = 0; k < C; ++k) ahead[i][k] = src[piece(first + WAVES * i) * (RW * D) + k];
   const Place at_ = place_of(args, tile, lane);
   if (row >= at_.count) return;
   int lo_any, hi_any, other;
@@ -697,35 +711,47 @@ __global__ void __launch_bounds__(kAttnThreads) kv_attention_join_kernel(AttnArg
   bounds_of(args, at_, at_.row0 + at_.count - 1, other, hi_any);
   const int n = cut_of(args, lo_any & ~31, hi_any).n;
   if (n == 1) return;  // its workgroup has written the result
-  const Parts parts = parts_of<D, RW>(args, tile, kvh);
-  const float2 none = make_float2(-__builtin_inff(), 0.0f);
-  static_assert(kMaxSplits == 128, "two pieces a lane");
-  const float2 x0 = lane < n ? parts.ml[lane * RW + row] : none;
-  const float2 x1 = lane + 64 < n ? parts.ml[(lane + 64) * RW + row] : none;
+  x0 = lane < n ? x0 : make_float2(-__builtin_inff(), 0.0f);
+  x1 = lane + 64 < n ? x1 : make_float2(-__builtin_inff(), 0.0f);
   float M = __builtin_fmaxf(x0.x, x1.x);
   for (int d = 1; d < 64; d <<= 1) M = __builtin_fmaxf(M, __shfl_xor(M, d));
   const float f0 = join_weight(x0.x, M), f1 = join_weight(x1.x, M);
   float L = f0 * x0.y + f1 * x1.y;
   for (int d = 1; d < 64; d <<= 1) L += __shfl_xor(L, d);
-  weight[wave][lane] = f0;
-  weight[wave][lane + 64] = f1;
-  __builtin_amdgcn_wave_barrier();  // one wavefront's LDS accesses stay in order
-  constexpr int C = D / 64;  // columns C lane .. of a lane
+  const auto weight = [&](int i) {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)u32(i < 64 ? f0 : f1), i & 63));
+  };
   float o[C] = {};
-  const float* src = parts.o + (size_t)row * D + C * lane;
-#pragma unroll 8
-  for (int s = 0; s < n; ++s) {
-    const float f = weight[wave][s];
 #pragma unroll
-    for (int i = 0; i < C; ++i) o[i] = __builtin_fmaf(f, src[(size_t)s * (RW * D) + i], o[i]);
+  for (int i = 0; i < AHEAD; ++i)
+    if (first + WAVES * i < n) {
+      const float f = weight(first + WAVES * i);
+#pragma unroll
+      for (int k = 0; k < C; ++k) o[k] = __builtin_fmaf(f, ahead[i][k], o[k]);
+    }
+#pragma unroll 8
+  for (int i = first + WAVES * AHEAD; i < n; i += WAVES) {
+    const float f = weight(i);
+#pragma unroll
+    for (int k = 0; k < C; ++k) o[k] = __builtin_fmaf(f, src[(size_t)i * (RW * D) + k], o[k]);
+  }
+  if constexpr (WAVES > 1) {
+#pragma unroll
+    for (int k = 0; k < C; ++k) part[wave][C * lane + k] = o[k];
+    __syncthreads();
+    if (wave != 0) return;
+#pragma unroll
+    for (int k = 0; k < C; ++k)
+#pragma unroll
+      for (int v = 1; v < WAVES; ++v) o[k] += part[v][C * lane + k];
   }
   const bool empty = M == -__builtin_inff() && L == 0.0f;
   const float inv = empty ? 0.0f : outer_alpha(a.cache.v_amax[kvh], a.cache.global_fp8_max) / L;
-  const int64_t at = out_row(args, at_, (int)kvh, row);
-  uint16_t* dst = a.out + at * D + C * lane;
+  const int64_t to = out_row(args, at_, (int)kvh, row);
+  uint16_t* dst = a.out + to * D + C * lane;
 #pragma unroll
-  for (int i = 0; i < C; ++i) dst[i] = empty ? (uint16_t)0 : (uint16_t)bf16_pair(o[i] * inv, 0.0f);
-  if (a.lse && lane == 0) a.lse[at] = empty ? -__builtin_inff() : (M + __builtin_log2f(L)) / kLog2e;
+  for (int k = 0; k < C; ++k) dst[k] = empty ? (uint16_t)0 : (uint16_t)bf16_pair(o[k] * inv, 0.0f);
+  if (a.lse && lane == 0) a.lse[to] = empty ? -__builtin_inff() : (M + __builtin_log2f(L)) / kLog2e;
 }
 
 // ---------------------------------------------------------------- many rows
@@ -933,10 +959,13 @@ AttnPlan kv_attention_plan(const nvfp4_kv_attention_args& a) {
     // keys and 8 heads: 2 pieces 92.8 us, 4 pieces 84.8; 16 requests of up to
     // 2000: 8 pieces 19.7, 4 pieces 16.4.
     const double C0 = 5, V = 60.0 * 128 / D, resident = (double)device_cu_count() * attn_waves(D, p.nq);
+    // tiles that an even batch has (p.tiles has room for any)
+    const int64_t even = a.tokens * group / p.rows;
+    const double likely = (double)((even > a.batch ? even : a.batch) * a.cache.kv_heads);
     const auto rounds = [&](double n) { return ceil(n / resident); };
     double best = 0;
     for (int n = 1; n <= kMaxSplits && (n - 1) * (int64_t)128 < keys; n += 1 + n / 16) {
-      const double piece = C0 + (double)keys / n / V, all = (double)groups * n;
+      const double piece = C0 + (double)keys / n / V, all = likely * n;
       const double cost = (rounds(all) + rounds(0.6 * all)) * piece + (n > 1 ? 6 + 0.1 * n : 0);
       if (n == 1 || cost < best) {
         best = cost;
@@ -958,11 +987,18 @@ static void launch_dim(const AttnArgs& x, const AttnPlan& p, hipStream_t s) {
     hipLaunchKernelGGL((kv_attention_rows_kernel<D, rows_nq(D)>), grid, block, 0, s, x);
     return;
   }
-  const dim3 rows((unsigned)(p.tiles * x.a.cache.kv_heads * (p.rows / 4)));
+  // rows that a tile can have
+  const int rows = !x.a.cu_q && x.group < p.rows ? x.group : p.rows;
   const auto launch = [&](auto nq) {
     constexpr int NQ = decltype(nq)::value;
     hipLaunchKernelGGL((kv_attention_keys_kernel<D, NQ>), grid, block, 0, s, x);
-    if (p.splits > 1) hipLaunchKernelGGL((kv_attention_join_kernel<D, 16 * NQ>), rows, block, 0, s, x);
+    if (p.splits == 1) return;
+    const int64_t tiles = p.tiles * x.a.cache.kv_heads;
+    if (p.splits >= kManyPieces)
+      hipLaunchKernelGGL((kv_attention_join_kernel<D, 16 * NQ, 4>), dim3((unsigned)(tiles * rows)), block, 0, s, x, rows);
+    else
+      hipLaunchKernelGGL((kv_attention_join_kernel<D, 16 * NQ, 1>), dim3((unsigned)(tiles * ((rows + 3) / 4))), block, 0,
+                         s, x, rows);
   };
   if (p.nq == 1) launch(std::integral_constant<int, 1>{});
   if constexpr (MOST >= 2) {
@@ -974,7 +1010,7 @@ static void launch_dim(const AttnArgs& x, const AttnPlan& p, hipStream_t s) {
 }
 
 hipError_t launch_kv_attention(const nvfp4_kv_attention_args& a, const AttnPlan& p, hipStream_t s) {
-  if (p.grid > INT32_MAX || p.tiles * a.cache.kv_heads * (p.rows / 4) > INT32_MAX) return hipErrorInvalidValue;
+  if (p.grid > INT32_MAX || p.tiles * a.cache.kv_heads * p.rows > INT32_MAX) return hipErrorInvalidValue;
   AttnArgs x = {};
   x.a = a;
   x.rows = p.rows;
