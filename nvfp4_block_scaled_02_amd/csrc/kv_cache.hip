@@ -80,6 +80,13 @@ kv_append_kernel(nvfp4_kv_append_args p, RowGrid grid) {
   const nvfp4_qk_args& a = p.qk;
   const nvfp4_kv_cache& c = p.cache;
   const int D = a.head_dim, heads = a.k_heads;
+  // the outer scales of the heads' keys and values, worked out once a workgroup
+  extern __shared__ float4 outer[];  // [2][heads]: alpha, K6, K4, whether it is unusable
+  for (int i = threadIdx.x; i < 2 * heads; i += kRowThreads) {
+    const TensorScale ts = tensor_scale(i < heads ? c.k_amax[i] : c.v_amax[i - heads], c.global_fp8_max);
+    outer[i] = make_float4(ts.alpha, ts.k6, ts.k4, ts.nan ? 1.0f : 0.0f);
+  }
+  __syncthreads();
   const RowMap<LPH> m(D, a.rot_dim, PAIRS);
   const Row8 wq = weight_load(a.q_weight, m), wk = weight_load(a.k_weight, m);
   const double inv_d = 1.0 / D, eps = a.eps;
@@ -97,45 +104,48 @@ kv_append_kernel(nvfp4_kv_append_args p, RowGrid grid) {
       if (m.active && h < a.q_heads) row_store(a.q_out + t.token * a.q_out_stride + h * D, m, y);
     });
     if (!stored) continue;  // the wavefront together
-    // quantizes a head's values under its outer amax and hands over the bytes
-    const auto quantize = [&](int h, const Row8& v, const float* amax, const auto& write) {
+    // where head 0 of the token lies; a head further is page_size tokens on
+    // (below 2^28 bytes for all of them)
+    const int64_t page_tokens = (slot >> shift) * heads << shift;
+    const int off = (int)(slot & (c.page_size - 1));
+    const int64_t kt = page_tokens + off, vt = page_tokens + (off & ~7);
+    uint8_t* kc = c.k_codes + kt * (D / 2);
+    uint8_t* ks = c.k_scales + kt * (D / 16);
+    uint8_t* vc = c.v_codes + vt * (D / 2) + (off & 7);
+    uint8_t* vs = c.v_scales + vt * (D / 16) + (off & 7);
+    const auto quantize = [&](int h, const Row8& v, int kind, uint32_t (&codes)[2], uint32_t (&scale)[2]) {
       float x[8];
       v.unpack(x);
-      const int hc = h < heads ? h : heads - 1;
-      uint32_t codes[2], scale[2];
-      quad_quantize<SELECT>(x, tensor_scale(amax[hc], c.global_fp8_max), codes, scale);
-      if (m.active && h < heads)
-        write(KvAddr{(slot >> shift) * heads + h, (int)(slot & (c.page_size - 1)), c.page_size, D}, codes, scale);
+      const float4 o = outer[kind * heads + (h < heads ? h : heads - 1)];
+      quad_quantize<SELECT>(x, TensorScale{o.x, o.y, o.z, o.w != 0.0f}, codes, scale);
     };
     const RowPart pk = part_of(t, grid.q_groups, grid.k_groups);
     row_walk(a.k + t.token * a.k_stride, heads, D, pk.g0, pk.g1, m, [&](int h, const Row8& v) {
-      quantize(h, row_norm_rope<LPH, PAIRS>(v, m, a.k_weight != nullptr, wk, eps, inv_d, ang), c.k_amax,
-               [&](const KvAddr& k, const uint32_t (&codes)[2], const uint32_t (&scale)[2]) {
-                 uint8_t* kc = c.k_codes + k.k_code();
-                 *reinterpret_cast<uint16_t*>(kc + m.e0 / 2) = (uint16_t)codes[0];
-                 *reinterpret_cast<uint16_t*>(kc + m.e1 / 2) = (uint16_t)codes[1];
-                 if ((threadIdx.x & 3) == 0) {
-                   uint8_t* ks = c.k_scales + k.k_scale();
-                   ks[m.e0 / 16] = (uint8_t)scale[0];
-                   ks[m.e1 / 16] = (uint8_t)scale[1];
-                 }
-               });
+      uint32_t codes[2], scale[2];
+      quantize(h, row_norm_rope<LPH, PAIRS>(v, m, a.k_weight != nullptr, wk, eps, inv_d, ang), 0, codes, scale);
+      if (!m.active || h >= heads) return;
+      const uint32_t at = ((uint32_t)h << shift) * (uint32_t)(D / 2), sat = ((uint32_t)h << shift) * (uint32_t)(D / 16);
+      *reinterpret_cast<uint16_t*>(kc + at + m.e0 / 2) = (uint16_t)codes[0];
+      *reinterpret_cast<uint16_t*>(kc + at + m.e1 / 2) = (uint16_t)codes[1];
+      if ((threadIdx.x & 3) == 0) {
+        ks[sat + m.e0 / 16] = (uint8_t)scale[0];
+        ks[sat + m.e1 / 16] = (uint8_t)scale[1];
+      }
     });
     const RowPart pv = part_of(t, grid.q_groups + grid.k_groups, grid.v_groups);
     row_walk(p.v + t.token * p.v_stride, heads, D, pv.g0, pv.g1, m, [&](int h, const Row8& v) {
-      quantize(h, v.or_zero(m.active), c.v_amax,
-               [&](const KvAddr& k, const uint32_t (&codes)[2], const uint32_t (&scale)[2]) {
-                 uint8_t* vc = c.v_codes + k.v_code();
-                 vc[8 * (m.e0 / 2)] = (uint8_t)codes[0];
-                 vc[8 * (m.e0 / 2 + 1)] = (uint8_t)(codes[0] >> 8);
-                 vc[8 * (m.e1 / 2)] = (uint8_t)codes[1];
-                 vc[8 * (m.e1 / 2 + 1)] = (uint8_t)(codes[1] >> 8);
-                 if ((threadIdx.x & 3) == 0) {
-                   uint8_t* vs = c.v_scales + k.v_scale();
-                   vs[8 * (m.e0 / 16)] = (uint8_t)scale[0];
-                   vs[8 * (m.e1 / 16)] = (uint8_t)scale[1];
-                 }
-               });
+      uint32_t codes[2], scale[2];
+      quantize(h, v.or_zero(m.active), 1, codes, scale);
+      if (!m.active || h >= heads) return;
+      const uint32_t at = ((uint32_t)h << shift) * (uint32_t)(D / 2), sat = ((uint32_t)h << shift) * (uint32_t)(D / 16);
+      vc[at + 4 * m.e0] = (uint8_t)codes[0];
+      vc[at + 4 * m.e0 + 8] = (uint8_t)(codes[0] >> 8);
+      vc[at + 4 * m.e1] = (uint8_t)codes[1];
+      vc[at + 4 * m.e1 + 8] = (uint8_t)(codes[1] >> 8);
+      if ((threadIdx.x & 3) == 0) {
+        vs[sat + m.e0 / 2] = (uint8_t)scale[0];
+        vs[sat + m.e1 / 2] = (uint8_t)scale[1];
+      }
     });
   }
 }
@@ -143,12 +153,13 @@ kv_append_kernel(nvfp4_kv_append_args p, RowGrid grid) {
 template <int LPH, int PAIRS>
 static hipError_t launch_append2(const nvfp4_kv_append_args& a, hipStream_t s) {
   const RowGrid g = row_grid_of(a.qk.tokens, LPH, a.qk.q_heads, a.qk.k_heads, a.qk.k_heads);
+  const size_t lds = 2 * (size_t)a.qk.k_heads * sizeof(float4);  // at most 32 KB
   if (a.select == NVFP4_SELECT_6)
     hipLaunchKernelGGL((kv_append_kernel<LPH, PAIRS, SELECT_6>), dim3(row_blocks(g)), dim3(kRowThreads),
-                       0, s, a, g);
+                       lds, s, a, g);
   else
     hipLaunchKernelGGL((kv_append_kernel<LPH, PAIRS, SELECT_4OVER6>), dim3(row_blocks(g)),
-                       dim3(kRowThreads), 0, s, a, g);
+                       dim3(kRowThreads), lds, s, a, g);
   return hipGetLastError();
 }
 
