@@ -322,6 +322,10 @@ struct Walk {
           if (!attends(n, key0 + i, w.ok)) s[n][i / 4][i % 4] = -__builtin_inff();
       hide_values(w, key0, lo_any, hi_any);
     }
+    float top[NQ];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) top[n] = top_of(n, s[n][0], s[n][1]);
+    raise(top);
     f16x8 p[NQ];
 #pragma unroll
     for (int n = 0; n < NQ; ++n) p[n] = weights(n, s[n][0], s[n][1]);
@@ -342,15 +346,24 @@ struct Walk {
     }
   }
 
-  // The softmax weights of query n's scores of a tile (binary16), added to
-  // its sum; its maximum moves first where a score passes it by 2^8.
-  __device__ __forceinline__ f16x8 weights(int n, const f32x4& s0, const f32x4& s1) {
-    // factor >= 0: the largest product is that of the largest score.  A NaN
-    // score never moves the maximum; its weight and the row become NaN.
-    const float top = factor[n] * max3(max3(s0[0], s0[1], s0[2]), max3(s0[3], s1[0], s1[1]), max3(s1[2], s1[3], s1[3]));
-    if (__any(top > thr[n])) {
+  // Largest score of query n among a lane's eight of a tile, as the exponent's
+  // argument (factor >= 0: the largest product is that of the largest score).
+  __device__ __forceinline__ float top_of(int n, const f32x4& s0, const f32x4& s1) const {
+    return factor[n] * max3(max3(s0[0], s0[1], s0[2]), max3(s0[3], s1[0], s1[1]), max3(s1[2], s1[3], s1[3]));
+  }
+  // Moves the maxima of all rows where a score passes one by 2^8.  A NaN score
+  // never does; its weight and the row become NaN.  One branch for all rows,
+  // so that what surrounds it stays in long runs that the matrix and the
+  // vector units share.
+  __device__ __forceinline__ void raise(const float (&top)[NQ]) {
+    bool passed = false;
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) passed |= top[n] > thr[n];
+    if (!__any(passed)) return;
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
       const float was = m[n];
-      m[n] = __builtin_fmaxf(m[n], max_over_g(top));
+      m[n] = __builtin_fmaxf(m[n], max_over_g(top[n]));
       thr[n] = m[n] + 8.0f;
       const float keep = was == m[n] || was == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(was - m[n]);
       l[n] *= keep;
@@ -359,6 +372,9 @@ struct Walk {
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[n][j][e] *= keep;
     }
+  }
+  // The softmax weights of query n's scores of a tile (binary16), added to its sum.
+  __device__ __forceinline__ f16x8 weights(int n, const f32x4& s0, const f32x4& s1) {
     const float base = m[n] == -__builtin_inff() ? 0.0f : -m[n];
     f16x8 p, ones;
 #pragma unroll
@@ -835,7 +851,7 @@ kv_attention_rows_kernel(AttnArgs args) {
       }
       const int flag = (__any(nan) ? 1 : 0) | (__all(x.ok) ? 0 : 2);
       if (lane == 0) flags[buf][wave] = flag;
-#pragma unroll
+  #pragma unroll
       for (int j = 0; j < NJ; ++j) {
         const f16x2 f[4] = {fp8_lo(x.vs[j].x), fp8_hi(x.vs[j].x), fp8_lo(x.vs[j].y), fp8_hi(x.vs[j].y)};
         f16x8 even, odd;
@@ -859,45 +875,63 @@ kv_attention_rows_kernel(AttnArgs args) {
       p = pn;
       if (mine && t < hi_any && t + BLOCK > lo_any) {
         const int flag = __builtin_amdgcn_readfirstlane(flags[buf][0] | flags[buf][1] | flags[buf][2] | flags[buf][3]);
+        constexpr int U = D * NQ <= 256 ? 2 : 1;  // 32-key tiles whose scores are held at once
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int tu = t + 32 * u, key0 = tu + 8 * g;
-          f32x4 s[NQ][2];
+        for (int u0 = 0; u0 < 2; u0 += U) {
+          f32x4 s[U][NQ][2];
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
+          for (int v = 0; v < U; ++v)
 #pragma unroll
-            for (int i = 0; i < NCH; ++i) {
-              const f16x8 key = ks[buf][u][k][i][lane];
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int i = 0; i < NCH; ++i) {
+                const f16x8 key = ks[buf][u0 + v][k][i][lane];
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+                  s[v][n][k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(key, w.q[n][i], i == 0 ? f32x4{0, 0, 0, 0} : s[v][n][k], 0, 0, 0);
+              }
+          const int tu = t + 32 * u0;
+          if (!(tu >= lo_all && tu + 32 * U <= hi_all) || flag) {
+#pragma unroll
+            for (int v = 0; v < U; ++v) {
+              const int tv = tu + 32 * v, key0 = tv + 8 * g;
+              const Pages pv = rd.pages(tv);
+              const bool ok = (uint32_t)pv.v < (uint32_t)c.num_pages;
 #pragma unroll
               for (int n = 0; n < NQ; ++n)
-                s[n][k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(key, w.q[n][i], i == 0 ? f32x4{0, 0, 0, 0} : s[n][k], 0, 0, 0);
-            }
-          if (!(tu >= lo_all && tu + 32 <= hi_all) || flag) {
-            const Pages pu = rd.pages(tu);
-            const bool ok = (uint32_t)pu.v < (uint32_t)c.num_pages;
 #pragma unroll
-            for (int n = 0; n < NQ; ++n)
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (!w.attends(n, key0 + i, ok)) s[n][i / 4][i % 4] = -__builtin_inff();
-            if (flag & 1) {  // NaN values: the rows that attend them
-              Raw<D> raw;
-              rd.load(tu, pu, raw);
-              w.hide_values(raw, key0, lo_any, hi_any);
+                for (int i = 0; i < 8; ++i)
+                  if (!w.attends(n, key0 + i, ok)) s[v][n][i / 4][i % 4] = -__builtin_inff();
+              if (flag & 1) {  // NaN values: the rows that attend them
+                Raw<D> raw;
+                rd.load(tv, pv, raw);
+                w.hide_values(raw, key0, lo_any, hi_any);
+              }
             }
           }
-          f16x8 pw[NQ];
+          float top[NQ];
 #pragma unroll
-          for (int n = 0; n < NQ; ++n) pw[n] = w.weights(n, s[n][0], s[n][1]);
+          for (int n = 0; n < NQ; ++n) {
+            top[n] = w.top_of(n, s[0][n][0], s[0][n][1]);
+            if constexpr (U == 2) top[n] = __builtin_elementwise_maximum(top[n], w.top_of(n, s[U - 1][n][0], s[U - 1][n][1]));
+          }
+          w.raise(top);
+          f16x8 pw[U][NQ];
 #pragma unroll
-          for (int j = 0; j < NJ; ++j)
+          for (int v = 0; v < U; ++v)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const f16x8 v = vs[buf][u][j][e][lane];
+            for (int n = 0; n < NQ; ++n) pw[v][n] = w.weights(n, s[v][n][0], s[v][n][1]);
 #pragma unroll
-              for (int n = 0; n < NQ; ++n)
-                w.o[n][j][e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pw[n], w.o[n][j][e], 0, 0, 0);
-            }
+          for (int v = 0; v < U; ++v)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const f16x8 value = vs[buf][u0 + v][j][e][lane];
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+                  w.o[n][j][e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(value, pw[v][n], w.o[n][j][e], 0, 0, 0);
+              }
         }
       }
       put(x, tn, buf ^ 1);

@@ -188,6 +188,46 @@ def test_nan_keys_and_values_reach_the_rows_that_attend_them():
     assert np.isnan(o_[40:45, :, 32:48]).all() and np.isfinite(o_[45:60]).all()
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_prompts_with_nan_and_bad_pages(d):
+    """The same in the form for many rows: NaN keys and values, missing pages
+    and garbage past the end, in tiles that rows attend in part."""
+    lens, new = [210, 150], [180, 140]
+    c = _make(lens, 16, 1, d, 20 + d)
+
+    def at(b, j):
+        return c["table"][b, j // 16], j % 16
+
+    qb = _queries(320, 2, d, 20)
+    p, o = at(0, 150)
+    c["vs"][p, 0, o // 8, 1, o % 8] = 0x7F
+    p, o = at(1, 60)
+    c["ks"][p, 0, o, 2] = 0x7F
+    o_, _ = _run(c, qb, lens, new)
+    assert np.isfinite(o_[:120]).all() and np.isnan(o_[120:180, :, 16:32]).all()
+    assert np.isfinite(o_[120:180, :, :16]).all() and np.isfinite(o_[180:230]).all() and np.isnan(o_[230:]).all()
+    _run(c, qb, lens, new, window=20)
+    _run(c, qb, lens, new, causal=False, window=33)
+    c["table"][0, 3], c["table"][0, 9], c["table"][1, 1] = -1, 1 << 29, len(c["kc"])
+    _run(c, qb, lens, new)
+    _run(c, qb, [100, 150], new)  # rows before the first token
+    c["table"][1, :] = -1
+    o_, l = _run(c, qb, lens, new)
+    assert (o_[180:] == 0).all() and np.isneginf(l[180:]).all()
+
+
+def test_many_requests_and_uneven_rows():
+    # more requests than one probe of 64 finds; prompts among single tokens
+    rng = np.random.default_rng(21)
+    new = rng.choice([0, 1, 1, 1, 3, 40], 300).tolist()
+    lens = [n + int(k) for n, k in zip(new, rng.integers(0, 60, 300))]
+    c = _make(lens, 8, 1, 64, 21)
+    _run(c, _queries(sum(new), 2, 64, 21), lens, new)
+    lens = rng.integers(0, 50, 700).tolist()
+    c = _make(lens, 8, 1, 64, 22)
+    _run(c, _queries(700, 2, 64, 22), lens, [1] * 700)
+
+
 def test_special_queries():
     lens = [50] * 6
     c = _make(lens, 16, 1, 128, 14)
@@ -219,6 +259,15 @@ def test_extreme_scales_and_amaxes():
     c["amax"][0][0] = np.nan
     o, _ = _run(c, _queries(2, 4, 64, 16, mult=1e-4), lens, [1, 1], check=False)
     assert np.isnan(o[:, :2]).all() and np.isfinite(o[:, 2:]).all()
+
+
+def test_wide_head_groups():
+    # more heads in a group than a tile has rows
+    lens = [70, 3, 200]
+    c = _make(lens, 16, 1, 128, 23)
+    _run(c, _queries(3, 48, 128, 23), lens, [1] * 3)
+    _run(c, _queries(3, 100, 128, 24), lens, [1] * 3)
+    _run(c, _queries(8, 24, 128, 25), lens, [5, 1, 2])
 
 
 def test_strided_queries_and_out():
