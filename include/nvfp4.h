@@ -701,7 +701,9 @@ int nvfp4_kv_read(const nvfp4_kv_cache* cache, const int64_t* slots, int64_t tok
  * sizes < 0, q_heads not a positive multiple of kv_heads or above
  * NVFP4_KV_MAX_HEADS, cu_q NULL with tokens != batch, scale not finite,
  * window < 0, batch, tokens, table_width or max_seq_len > 2^31 - 1;
- * NVFP4_ERR_UNSUPPORTED: table_width * page_size > 2^30 or tokens * q_heads > 2^31.
+ * NVFP4_ERR_UNSUPPORTED: table_width * page_size > 2^30, tokens * q_heads >
+ * 2^31, or more than 2^24 - 1 workgroups, of which every key/value head has
+ * one for 16 to 256 query rows of a request.
  */
 typedef struct nvfp4_kv_attention_args {
   const uint16_t* q;

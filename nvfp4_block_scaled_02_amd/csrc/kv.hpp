@@ -19,6 +19,8 @@ size_t qk_norm_rope_bwd_workspace(int head_dim);
 hipError_t launch_kv_append(const nvfp4_kv_append_args& a, hipStream_t s);
 hipError_t launch_kv_read(const nvfp4_kv_cache& c, const int64_t* slots, int64_t tokens,
                           uint16_t* k_out, uint16_t* v_out, hipStream_t s);
+constexpr int64_t kAttnMaxGroups = (1 << 24) - 1;
+
 // Launch shape of an attention call, from its sizes alone.
 struct AttnPlan {
   int nq;           // 16-row tiles of a wavefront

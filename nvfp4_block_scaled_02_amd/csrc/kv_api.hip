@@ -170,6 +170,8 @@ static int attention_ok(const nvfp4_kv_attention_args& a) {
   if (st == NVFP4_OK && (a.table_width > ((int64_t)1 << 30) / a.cache.page_size ||
                          a.tokens > ((int64_t)1 << 31) / a.q_heads))
     return NVFP4_ERR_UNSUPPORTED;
+  // threads of one launch stay in 32 bits
+  if (st == NVFP4_OK && kv_attention_plan(a).grid > kAttnMaxGroups) return NVFP4_ERR_UNSUPPORTED;
   return st;
 }
 

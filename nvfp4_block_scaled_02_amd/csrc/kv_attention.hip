@@ -981,7 +981,8 @@ AttnPlan kv_attention_plan(const nvfp4_kv_attention_args& a) {
                    : a.batch * ((group + p.rows - 1) / p.rows);
   const int64_t groups = p.tiles * a.cache.kv_heads;
   int64_t keys = a.max_seq_len;
-  if (a.window > 0 && a.window + p.rows / group + 64 < keys) keys = a.window + p.rows / group + 64;
+  const int64_t reach = p.rows / group + 64;  // of a tile's rows and blocks, beyond the window
+  if (a.window > 0 && a.window < keys - reach) keys = a.window + reach;
   p.splits = 1;
   p.chunk = 0x7FFFFF80;
   if (!p.rows_split && keys > 128) {
@@ -998,7 +999,9 @@ AttnPlan kv_attention_plan(const nvfp4_kv_attention_args& a) {
     const double likely = (double)((even > a.batch ? even : a.batch) * a.cache.kv_heads);
     const auto rounds = [&](double n) { return ceil(n / resident); };
     double best = 0;
-    for (int n = 1; n <= kMaxSplits && (n - 1) * (int64_t)128 < keys; n += 1 + n / 16) {
+    // past 16 rounds there is nothing left to even out, only workspace to fill
+    for (int n = 1; n == 1 || (n <= kMaxSplits && (n - 1) * (int64_t)128 < keys && likely * n <= 16 * resident);
+         n += 1 + n / 16) {
       const double piece = C0 + (double)keys / n / V, all = likely * n;
       const double cost = (rounds(all) + rounds(0.6 * all)) * piece + (n > 1 ? 6 + 0.1 * n : 0);
       if (n == 1 || cost < best) {
@@ -1044,9 +1047,9 @@ static void launch_dim(const AttnArgs& x, const AttnPlan& p, hipStream_t s) {
 }
 
 hipError_t launch_kv_attention(const nvfp4_kv_attention_args& a, const AttnPlan& p, hipStream_t s) {
-  if (p.grid > INT32_MAX || p.tiles * a.cache.kv_heads * p.rows > INT32_MAX) return hipErrorInvalidValue;
   AttnArgs x = {};
   x.a = a;
+  if (x.a.window > INT32_MAX) x.a.window = 0;  // reaches past every position
   x.rows = p.rows;
   x.splits = p.splits;
   x.chunk = p.chunk;

@@ -233,7 +233,8 @@ inline RowGrid row_grid_of(int64_t tokens, int lph, int q_heads, int k_heads, in
   return g;
 }
 inline unsigned row_blocks(const RowGrid& g) {
-  const int64_t n = (g.waves + 3) / 4, cap = (int64_t)1 << 30;
+  // threads of one launch stay in 32 bits; more work makes the workgroups walk
+  const int64_t n = (g.waves + 3) / 4, cap = (int64_t)1 << 23;
   return (unsigned)(n < cap ? n : cap);
 }
 

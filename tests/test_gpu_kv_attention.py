@@ -371,3 +371,14 @@ def test_refusals():
         with pytest.raises(nv._native.NativeError):
             bad()
     assert nv.kv_attention(q[:0], cache, table[:0], lens[:0]).shape == (0, 4, 64)
+
+
+def test_window_past_every_position():
+    """A window wider than any sequence attends as none does, to the last bit."""
+    c = _make([700, 3, 90], 16, 2, 128, 71)
+    qb = _queries(3 + 40, 8, 128, 71)
+    for new in ([1, 1, 1], [40, 2, 1]):
+        n = sum(new)
+        runs = [_run(c, qb[:n], [700, 3, 90], new, window=w, check=w == 0) for w in (0, 2**31 - 1, 2**31, 2**63 - 1)]
+        for o, l in runs[1:]:
+            assert np.array_equal(o, runs[0][0]) and np.array_equal(l, runs[0][1])
