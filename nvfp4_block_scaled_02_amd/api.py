@@ -125,12 +125,13 @@ _CAPTURE = threading.local()
 def _invoke(entry: str, args: tuple, device, keep):
     """Issues entry(*args, stream) on the current stream of `device` now, or,
     inside prepare(), records it as a Launch instead."""
-    launch = Launch(entry, args, device, keep)
     rec = getattr(_CAPTURE, "launches", None)
     if rec is not None:
-        rec.append(launch)
-    else:
-        launch()
+        rec.append(Launch(entry, args, device, keep))
+        return
+    st = getattr(N.lib(), entry)(*args, _stream(device))
+    if st != N.OK:
+        N.check(st, entry)
 
 
 def prepare(fn, *args, **kwargs):

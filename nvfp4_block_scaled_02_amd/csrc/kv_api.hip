@@ -153,7 +153,7 @@ int nvfp4_kv_read(const nvfp4_kv_cache* cache, const int64_t* slots, int64_t tok
   return status_of(launch_kv_read(*cache, slots, tokens, k_out, v_out, stream));
 }
 
-static int attention_ok(const nvfp4_kv_attention_args& a) {
+static int attention_ok(const nvfp4_kv_attention_args& a, AttnPlan& plan) {
   const int st = cache_ok(a.cache);
   if (st == NVFP4_ERR_INVALID) return st;
   if (a.tokens < 0 || a.tokens > kMax32 || a.batch < 0 || a.batch > kMax32 || a.table_width < 0 ||
@@ -170,20 +170,22 @@ static int attention_ok(const nvfp4_kv_attention_args& a) {
   if (st == NVFP4_OK && (a.table_width > ((int64_t)1 << 30) / a.cache.page_size ||
                          a.tokens > ((int64_t)1 << 31) / a.q_heads))
     return NVFP4_ERR_UNSUPPORTED;
+  if (st != NVFP4_OK) return st;
+  plan = kv_attention_plan(a);
   // threads of one launch stay in 32 bits
-  if (st == NVFP4_OK && kv_attention_plan(a).grid > kAttnMaxGroups) return NVFP4_ERR_UNSUPPORTED;
-  return st;
+  return plan.grid > kAttnMaxGroups ? NVFP4_ERR_UNSUPPORTED : NVFP4_OK;
 }
 
 size_t nvfp4_kv_attention_workspace_bytes(const nvfp4_kv_attention_args* args) {
-  if (!args || attention_ok(*args) != NVFP4_OK) return 0;
-  return kv_attention_plan(*args).bytes;
+  AttnPlan plan = {};
+  return !args || attention_ok(*args, plan) != NVFP4_OK ? 0 : plan.bytes;
 }
 
 int nvfp4_kv_attention(const nvfp4_kv_attention_args* args, hipStream_t stream) {
   if (!args) return NVFP4_ERR_INVALID;
   const nvfp4_kv_attention_args& a = *args;
-  const int st = attention_ok(a);
+  AttnPlan plan = {};
+  const int st = attention_ok(a, plan);
   if (st == NVFP4_ERR_INVALID) return st;
   if (a.tokens > 0 && (!given(a.q, 16) || !given(a.out, 16))) return NVFP4_ERR_INVALID;
   if (!aligned(a.lse, 4) || !aligned(a.cu_q, 4) || !aligned(a.workspace, 16)) return NVFP4_ERR_INVALID;
@@ -191,7 +193,6 @@ int nvfp4_kv_attention(const nvfp4_kv_attention_args* args, hipStream_t stream) 
     return NVFP4_ERR_INVALID;
   if (st != NVFP4_OK) return st;
   if (a.tokens == 0) return NVFP4_OK;
-  const AttnPlan plan = kv_attention_plan(a);
   if (plan.bytes != 0 && !a.workspace) return NVFP4_ERR_INVALID;
   return status_of(launch_kv_attention(a, plan, stream));
 }

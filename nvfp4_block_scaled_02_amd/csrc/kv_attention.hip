@@ -993,17 +993,18 @@ AttnPlan kv_attention_plan(const nvfp4_kv_attention_args& a) {
     // requests of 0.6 of the bound.  Measured at 64 requests of 1024 to 8192
     // keys and 8 heads: 2 pieces 92.8 us, 4 pieces 84.8; 16 requests of up to
     // 2000: 8 pieces 19.7, 4 pieces 16.4.
-    const double C0 = 5, V = 60.0 * 128 / D, resident = (double)device_cu_count() * attn_waves(D, p.nq);
+    const double C0 = 5, V = 60.0 * 128 / D;
+    const int64_t resident = (int64_t)device_cu_count() * attn_waves(D, p.nq);
     // tiles that an even batch has (p.tiles has room for any)
     const int64_t even = a.tokens * group / p.rows;
-    const double likely = (double)((even > a.batch ? even : a.batch) * a.cache.kv_heads);
-    const auto rounds = [&](double n) { return ceil(n / resident); };
+    const int64_t likely = (even > a.batch ? even : a.batch) * a.cache.kv_heads;
     double best = 0;
     // past 16 rounds there is nothing left to even out, only workspace to fill
     for (int n = 1; n == 1 || (n <= kMaxSplits && (n - 1) * (int64_t)128 < keys && likely * n <= 16 * resident);
          n += 1 + n / 16) {
-      const double piece = C0 + (double)keys / n / V, all = likely * n;
-      const double cost = (rounds(all) + rounds(0.6 * all)) * piece + (n > 1 ? 6 + 0.1 * n : 0);
+      const int64_t all = likely * n;
+      const int64_t rounds = (all + resident - 1) / resident + (3 * all + 5 * resident - 1) / (5 * resident);
+      const double cost = (double)rounds * (C0 + (double)keys / (n * V)) + (n > 1 ? 6 + 0.1 * n : 0);
       if (n == 1 || cost < best) {
         best = cost;
         p.splits = n;
