@@ -105,15 +105,19 @@ struct Pages {
 };
 
 // A byte holds two columns of one token; the products want 8 tokens of one
-// column.  x, y: the bytes of tokens 0..3 and 4..7 of a column pair; nibbles of
-// neighbouring bytes change places, and a conversion takes two tokens at once.
+// column, in any order that the weights share.  x, y: the bytes of tokens 0..3
+// and 4..7 of a column pair; one column's nibbles of y move beside x's, and a
+// conversion takes tokens i and i + 4 at once: the order 0 4 1 5 2 6 3 7.
 __device__ __forceinline__ void value_columns(uint32_t x, uint32_t y, const f16x2 (&f)[4], f16x8& even, f16x8& odd) {
-  const uint32_t M = 0x000F000Fu;
-  const uint32_t x4 = x >> 4, y4 = y >> 4, x8 = x >> 8, y8 = y >> 8;
-  const uint32_t xe = (x & M) | (x4 & ~M), ye = (y & M) | (y4 & ~M);
-  const uint32_t xo = (x4 & M) | (x8 & ~M), yo = (y4 & M) | (y8 & ~M);
-  even = join8(fp4_pair(xe, 0) * f[0], fp4_pair(xe, 2) * f[1], fp4_pair(ye, 0) * f[2], fp4_pair(ye, 2) * f[3]);
-  odd = join8(fp4_pair(xo, 0) * f[0], fp4_pair(xo, 2) * f[1], fp4_pair(yo, 0) * f[2], fp4_pair(yo, 2) * f[3]);
+  const uint32_t M = 0x0F0F0F0Fu;
+  const uint32_t e = (x & M) | ((y << 4) & ~M), o = ((x >> 4) & M) | (y & ~M);
+  even = join8(fp4_pair(e, 0) * f[0], fp4_pair(e, 1) * f[1], fp4_pair(e, 2) * f[2], fp4_pair(e, 3) * f[3]);
+  odd = join8(fp4_pair(o, 0) * f[0], fp4_pair(o, 1) * f[1], fp4_pair(o, 2) * f[2], fp4_pair(o, 3) * f[3]);
+}
+// The tokens' block scales in that order.
+__device__ __forceinline__ void value_scales(uint2 s, f16x2 (&f)[4]) {
+  const uint32_t a = __builtin_amdgcn_perm(s.y, s.x, 0x05010400u), b = __builtin_amdgcn_perm(s.y, s.x, 0x07030602u);
+  f[0] = fp8_lo(a); f[1] = fp8_hi(a); f[2] = fp8_lo(b); f[3] = fp8_hi(b);
 }
 
 // Byte mask of the keys key0 .. key0 + 7 that lie in [lo, hi), on a page of
@@ -339,8 +343,8 @@ struct Walk {
     for (int n = 0; n < NQ; ++n) p[n] = weights(n, s[n][0], s[n][1]);
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      const uint2 vs = w.vs[j];
-      const f16x2 f[4] = {fp8_lo(vs.x), fp8_hi(vs.x), fp8_lo(vs.y), fp8_hi(vs.y)};
+      f16x2 f[4];
+      value_scales(w.vs[j], f);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         f16x8 ve, vo;
@@ -381,13 +385,14 @@ struct Walk {
         for (int e = 0; e < 4; ++e) o[n][j][e] *= keep;
     }
   }
-  // The softmax weights of query n's scores of a tile (binary16), added to its sum.
+  // The softmax weights of query n's scores of a tile (binary16, in the order of
+  // value_columns), added to its sum.
   __device__ __forceinline__ f16x8 weights(int n, const f32x4& s0, const f32x4& s1) {
     const float base = m[n] == -__builtin_inff() ? 0.0f : -m[n];
     f16x8 p, ones;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      p[i] = (_Float16)__builtin_amdgcn_exp2f(__builtin_fmaf(i < 4 ? s0[i % 4] : s1[i % 4], factor[n], base));
+      p[i] = (_Float16)__builtin_amdgcn_exp2f(__builtin_fmaf(i % 2 == 0 ? s0[i / 2] : s1[i / 2], factor[n], base));
       ones[i] = (_Float16)1.0f;
     }
     // the sum over the tile's keys, of the weights as they are used
@@ -861,7 +866,8 @@ kv_attention_rows_kernel(AttnArgs args) {
       if (lane == 0) flags[buf][wave] = flag;
   #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        const f16x2 f[4] = {fp8_lo(x.vs[j].x), fp8_hi(x.vs[j].x), fp8_lo(x.vs[j].y), fp8_hi(x.vs[j].y)};
+        f16x2 f[4];
+        value_scales(x.vs[j], f);
         f16x8 even, odd;
         value_columns(x.v[j].x, x.v[j].y, f, even, odd);
         vs[buf][half][j][2 * sub][lane] = even;
