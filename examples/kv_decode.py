@@ -41,6 +41,8 @@ class Layer:
         self.ctx, self.table = ints(requests), ints(requests, width)
         self.free = torch.arange(self.pages, dtype=torch.int32, device=device)
         self.count = torch.full((1,), self.pages, dtype=torch.int32, device=device)
+        # the layer's own, as its steps are captured: long sequences are joined in one launch
+        self.counters = torch.zeros(nv.KV_COUNTER_BYTES, dtype=torch.uint8, device=device)
 
     def step(self, x, new, one_each):
         """x [tokens, hidden] bf16: the requests' new tokens one after another
@@ -51,7 +53,8 @@ class Layer:
         q, k, v = y.split((HEADS, KV_HEADS, KV_HEADS), 1)  # views: nothing is copied
         q = nv.kv_append(self.cache, k, v, p.slots, q=q, positions=p.positions, cos=self.cos,
                          sin=self.sin, q_weight=self.q_weight, k_weight=self.k_weight)
-        out = nv.kv_attention(q, self.cache, self.table, p.seq_lens, None if one_each else p.cu_new)
+        out = nv.kv_attention(q, self.cache, self.table, p.seq_lens, None if one_each else p.cu_new,
+                              counters=self.counters)
         self.ctx.copy_(p.seq_lens)
         self.count.copy_(p.free_count)
         self.q = q

@@ -509,6 +509,7 @@ int nvfp4_dequantize_rht(const uint8_t* codes, const uint8_t* scales, int64_t ro
  * no operator uses a token outside the lengths it is given.
  */
 #define NVFP4_KV_MAX_HEADS 1024
+#define NVFP4_KV_COUNTER_BYTES 131072
 
 typedef struct nvfp4_kv_cache {
   uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
@@ -695,8 +696,12 @@ int nvfp4_kv_read(const nvfp4_kv_cache* cache, const int64_t* slots, int64_t tok
  *             aligned, with any contents; may be NULL where that size is 0.
  *             Overlapping calls need their own.  The bytes depend on tokens,
  *             batch, max_seq_len, heads, D, window and whether cu_q is given.
- * At most two launches: long key ranges are split over workgroups, and a
- * second launch joins the pieces in order.
+ *   counters  optional NVFP4_KV_COUNTER_BYTES, 16-byte aligned, zero-filled
+ *             once (every completed call leaves them zero); overlapping calls
+ *             need their own.
+ * Long key ranges are split over workgroups and the pieces joined in order: in
+ * the same launch where there are counters and few pieces, else by a second
+ * one; the bits are the same.
  * Errors (NVFP4_ERR_INVALID): the cache's rules, NULL or misaligned pointers,
  * sizes < 0, q_heads not a positive multiple of kv_heads or above
  * NVFP4_KV_MAX_HEADS, cu_q NULL with tokens != batch, scale not finite,
@@ -721,6 +726,7 @@ typedef struct nvfp4_kv_attention_args {
   uint16_t* out;
   float* lse;
   void* workspace;
+  void* counters;                     /* or NULL */
 } nvfp4_kv_attention_args;
 
 size_t nvfp4_kv_attention_workspace_bytes(const nvfp4_kv_attention_args* args);

@@ -9,13 +9,13 @@ from .api import (Launch, Quantized, default_global_max, dequantize, dequantize_
                   quantize_2d, quantize_pertoken, quantize_rht, quantize_rowscaled, requantize_t,
                   rht_amax, row_amax, tensor_amax, workspace, prepare, prepare_quantize,
                   prepare_dequantize, prepare_tensor_amax)
-from .kv import (KVCache, KVPlan, kv_append, kv_attention, kv_cache, kv_plan, kv_read,
+from .kv import (KV_COUNTER_BYTES, KVCache, KVPlan, kv_append, kv_attention, kv_cache, kv_plan, kv_read,
                  qk_norm_rope, qk_norm_rope_bwd, rope_table)
 
 __all__ = ["Launch", "Quantized", "default_global_max", "dequantize", "dequantize_rowscaled",
            "dequantize_rht", "dequantized_amax", "fakequant_bwd", "fakequant_fwd", "quantize",
            "quantize_2d", "quantize_pertoken", "quantize_rht", "quantize_rowscaled", "requantize_t",
            "rht_amax", "row_amax", "tensor_amax", "workspace", "prepare", "prepare_quantize",
-           "prepare_dequantize", "prepare_tensor_amax", "KVCache", "KVPlan", "kv_append",
+           "prepare_dequantize", "prepare_tensor_amax", "KV_COUNTER_BYTES", "KVCache", "KVPlan", "kv_append",
            "kv_attention", "kv_cache", "kv_plan", "kv_read", "qk_norm_rope", "qk_norm_rope_bwd",
            "rope_table"]

@@ -38,6 +38,7 @@ class QuantArgs(ctypes.Structure):
 
 
 PAIRS_HALVES, PAIRS_NEIGHBOURS = 0, 1
+KV_COUNTER_BYTES = 131072
 
 
 class KVCacheArgs(ctypes.Structure):
@@ -77,7 +78,7 @@ class KVAttentionArgs(ctypes.Structure):
                 ("cache", KVCacheArgs), ("block_table", _vp), ("batch", _i64),
                 ("table_width", _i64), ("seq_lens", _vp), ("cu_q", _vp), ("max_seq_len", _i64),
                 ("scale", _f32), ("causal", _int), ("window", _i64), ("out", _vp), ("lse", _vp),
-                ("workspace", _vp)]
+                ("workspace", _vp), ("counters", _vp)]
 
 
 _qa = ctypes.POINTER(QuantArgs)

@@ -27,6 +27,7 @@ struct AttnPlan {
   bool rows_split;  // wavefronts take rows of their own (else every fourth key tile)
   int rows;         // rows of a workgroup
   int splits;       // most workgroups over one tile's keys
+  bool join;        // pieces are joined in the same launch
   int chunk;        // keys a workgroup is meant to take
   int64_t tiles;    // row tiles over all requests, at most
   int64_t grid;

@@ -188,7 +188,8 @@ int nvfp4_kv_attention(const nvfp4_kv_attention_args* args, hipStream_t stream) 
   const int st = attention_ok(a, plan);
   if (st == NVFP4_ERR_INVALID) return st;
   if (a.tokens > 0 && (!given(a.q, 16) || !given(a.out, 16))) return NVFP4_ERR_INVALID;
-  if (!aligned(a.lse, 4) || !aligned(a.cu_q, 4) || !aligned(a.workspace, 16)) return NVFP4_ERR_INVALID;
+  if (!aligned(a.lse, 4) || !aligned(a.cu_q, 4) || !aligned(a.workspace, 16) || !aligned(a.counters, 16))
+    return NVFP4_ERR_INVALID;
   if (a.batch > 0 && (!given(a.seq_lens, 4) || (a.table_width > 0 && !given(a.block_table, 4))))
     return NVFP4_ERR_INVALID;
   if (st != NVFP4_OK) return st;

@@ -25,8 +25,8 @@
 //
 // Few rows (decoding, drafted tokens): the four wavefronts of a workgroup
 // take every fourth tile and join through LDS, and long key ranges are split
-// over workgroups whose partial results (binary32) a second launch joins in
-// order.  Many rows (prompts): each
+// over workgroups whose partial results (binary32) are joined in order, by the
+// last of them or by a second launch.  Many rows (prompts): each
 // wavefront has rows of its own, and the workgroup dequantizes each block of
 // keys once, into LDS.
 //
@@ -48,6 +48,8 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kAttnThreads = 256;
 constexpr int kMaxSplits = 128;
+constexpr int kManyPieces = 16;
+constexpr int kJoinCounters = NVFP4_KV_COUNTER_BYTES / 128;
 constexpr int kSlabStride = 68;  // floats of a 64-column slab row: 4 apart in the banks
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -55,6 +57,7 @@ struct AttnArgs {
   nvfp4_kv_attention_args a;
   int rows, splits, chunk, shift, group;
   uint32_t tiles, tiles_per_request;
+  int join;  // the last workgroup of a tile to finish joins its pieces
 };
 
 // ---------------------------------------------------------------- lanes
@@ -545,6 +548,118 @@ __device__ __forceinline__ float join_weight(float m, float M) {
   return m == M ? 1.0f : __builtin_amdgcn_exp2f(m - M);
 }
 
+// The weights of a row's pieces: lane i those of pieces i and i + 64, from
+// their (maximum, sum) pairs.
+struct Weights {
+  float f0, f1, M, L;
+  __device__ __forceinline__ Weights(float2 x0, float2 x1, int lane, int n) {
+    x0 = lane < n ? x0 : make_float2(-__builtin_inff(), 0.0f);
+    x1 = lane + 64 < n ? x1 : make_float2(-__builtin_inff(), 0.0f);
+    M = __builtin_fmaxf(x0.x, x1.x);
+    for (int d = 1; d < 64; d <<= 1) M = __builtin_fmaxf(M, __shfl_xor(M, d));
+    f0 = join_weight(x0.x, M);
+    f1 = join_weight(x1.x, M);
+    L = f0 * x0.y + f1 * x1.y;
+    for (int d = 1; d < 64; d <<= 1) L += __shfl_xor(L, d);
+  }
+  __device__ __forceinline__ float operator()(int i) const {
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)u32(i < 64 ? f0 : f1), i & 63));
+  }
+};
+// A joined row (columns C lane ..) and its lse.
+template <int D>
+__device__ __forceinline__ void put_row(const AttnArgs& args, const Place& at_, uint32_t kvh, int row, int lane,
+                                        const float (&o)[D / 64], const Weights& w) {
+  const nvfp4_kv_attention_args& a = args.a;
+  constexpr int C = D / 64;
+  const bool empty = w.M == -__builtin_inff() && w.L == 0.0f;
+  const float inv = empty ? 0.0f : outer_alpha(a.cache.v_amax[kvh], a.cache.global_fp8_max) / w.L;
+  const int64_t to = out_row(args, at_, (int)kvh, row);
+  uint16_t* dst = a.out + to * D + C * lane;
+#pragma unroll
+  for (int k = 0; k < C; ++k) dst[k] = empty ? (uint16_t)0 : (uint16_t)bf16_pair(o[k] * inv, 0.0f);
+  if (a.lse && lane == 0) a.lse[to] = empty ? -__builtin_inff() : (w.M + __builtin_log2f(w.L)) / kLog2e;
+}
+
+// Values that another workgroup of the launch reads: written and read at the
+// level that the whole GPU sees, so no cache is written back or emptied.
+__device__ __forceinline__ void put_shared(float* p, float x, float y) {
+  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), (uint64_t)u32(y) << 32 | u32(x), __ATOMIC_RELAXED,
+                     __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float2 get_shared(const float2* p) {
+  const uint64_t v = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+}
+__device__ __forceinline__ float get_shared(const float* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// After a workgroup's piece is on its way: true in the last of a tile's n to
+// arrive, which then sees all of them.  Nobody waits for anybody.
+__device__ __forceinline__ bool last_piece(const AttnArgs& args, uint32_t tile, uint32_t kvh, int n) {
+  __shared__ bool last;
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the piece has arrived
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    uint32_t* c = static_cast<uint32_t*>(args.a.counters) + 32 * (size_t)(tile * (uint32_t)args.a.cache.kv_heads + kvh);
+    last = __hip_atomic_fetch_add(c, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)n - 1;
+    if (last) __hip_atomic_store(c, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  return last;
+}
+
+// Joins a tile's n pieces, a wavefront per row, in the order of the kernel
+// below: SUMS sums of every SUMS-th piece.
+template <int D, int RW, int SUMS>
+__device__ __forceinline__ void join_here(const AttnArgs& args, const Place& at_, uint32_t kvh, const Parts& parts, int n) {
+  constexpr int C = D / 64;
+  const int lane = threadIdx.x & 63;
+  for (int row = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); row < at_.count; row += 4) {
+    const auto pair = [&](int i) { return get_shared(parts.ml + (size_t)(i < n ? i : n - 1) * RW + row); };
+    const float2 x0 = pair(lane), x1 = pair(lane + 64);
+    const float* src = parts.o + (size_t)row * D + C * lane;
+    const auto value = [&](int i, float (&y)[C]) {
+      const float* p = src + (size_t)(i < n ? i : n - 1) * (RW * D);
+      if constexpr (C % 2 == 0) {
+#pragma unroll
+        for (int k = 0; k < C; k += 2) {
+          const float2 v = get_shared(reinterpret_cast<const float2*>(p + k));
+          y[k] = v.x; y[k + 1] = v.y;
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < C; ++k) y[k] = get_shared(p + k);
+      }
+    };
+    constexpr int AHEAD = 8;
+    static_assert(AHEAD % SUMS == 0, "piece i belongs to sum i % SUMS");
+    float y[AHEAD][C], o[SUMS][C] = {};
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) value(u, y[u]);
+    const Weights w(x0, x1, lane, n);
+    for (int i = 0; i < n; i += AHEAD) {
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        if (i + u < n) {
+          const float f = w(i + u);
+#pragma unroll
+          for (int k = 0; k < C; ++k) o[u % SUMS][k] = __builtin_fmaf(f, y[u][k], o[u % SUMS][k]);
+        }
+      }
+      if (i + AHEAD < n)
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) value(i + AHEAD + u, y[u]);
+    }
+#pragma unroll
+    for (int v = 1; v < SUMS; ++v)
+#pragma unroll
+      for (int k = 0; k < C; ++k) o[0][k] += o[v][k];
+    put_row<D>(args, at_, kvh, row, lane, o[0], w);
+  }
+}
+
 // Wavefronts of a SIMD that the registers are shared out for: as many as fit
 // without spilling (512 registers a lane at one wavefront).
 constexpr int attn_waves(int D, int NQ) {
@@ -691,10 +806,21 @@ kv_attention_keys_kernel(AttnArgs args) {
           if (a.lse && j == 0 && col == 0) a.lse[at] = empty ? -__builtin_inff() : (M + __builtin_log2f(L)) / kLog2e;
         } else {
           const int at = (int)split * RW + row;
-          *reinterpret_cast<float4*>(parts.o + (size_t)at * D + 64 * j + col) = x;
-          if (j == 0 && col == 0) parts.ml[at] = make_float2(M, L);
+          float* dst = parts.o + (size_t)at * D + 64 * j + col;
+          if (args.join) {
+            put_shared(dst, x.x, x.y);
+            put_shared(dst + 2, x.z, x.w);
+            if (j == 0 && col == 0) put_shared(reinterpret_cast<float*>(parts.ml + at), M, L);
+          } else {
+            *reinterpret_cast<float4*>(dst) = x;
+            if (j == 0 && col == 0) parts.ml[at] = make_float2(M, L);
+          }
         }
       }
+    }
+    if (args.join && nsplit > 1 && last_piece(args, tile, kvh, nsplit)) {
+      if (args.splits >= kManyPieces) join_here<D, RW, 4>(args, at_, kvh, parts, nsplit);
+      else join_here<D, RW, 1>(args, at_, kvh, parts, nsplit);
     }
   }
 }
@@ -703,12 +829,11 @@ kv_attention_keys_kernel(AttnArgs args) {
 // pieces, a workgroup per row, each wavefront taking every fourth piece (16 of
 // them and more: one token over 8191 13.6 -> 11.9 us, 3 x 4 drafted tokens over
 // up to 131072 99 -> 90; 8 x 8 over up to 8192, few pieces, 40 against 52 the
-// other way).  A launch of its own: joined by the last workgroup of a tile to
-// arrive instead, the pieces of one tile pass through one CU (32 rows x 128
-// pieces: 257 us in all against 119).  What a piece holds is asked for before
-// it is known how many there are (the workspace has room for the most), so one
-// memory latency covers both.
-constexpr int kManyPieces = 16;
+// other way).  A launch of its own, where there are no counters or much to
+// join: by the last workgroup of a tile to arrive, the pieces of one tile pass
+// through one CU (32 rows x 128 pieces: 257 us in all against 119).  What a
+// piece holds is asked for before it is known how many there are (the
+// workspace has room for the most), so one memory latency covers both.
 template <int D, int RW, int WAVES>
 __global__ void __launch_bounds__(kAttnThreads) kv_attention_join_kernel(AttnArgs args, int rows) {
   __shared__ float part[WAVES == 1 ? 1 : WAVES][D];
@@ -740,16 +865,7 @@ __global__ void __launch_bounds__(kAttnThreads) kv_attention_join_kernel(AttnArg
   bounds_of(args, at_, at_.row0 + at_.count - 1, other, hi_any);
   const int n = cut_of(args, lo_any & ~31, hi_any).n;
   if (n == 1) return;  // its workgroup has written the result
-  x0 = lane < n ? x0 : make_float2(-__builtin_inff(), 0.0f);
-  x1 = lane + 64 < n ? x1 : make_float2(-__builtin_inff(), 0.0f);
-  float M = __builtin_fmaxf(x0.x, x1.x);
-  for (int d = 1; d < 64; d <<= 1) M = __builtin_fmaxf(M, __shfl_xor(M, d));
-  const float f0 = join_weight(x0.x, M), f1 = join_weight(x1.x, M);
-  float L = f0 * x0.y + f1 * x1.y;
-  for (int d = 1; d < 64; d <<= 1) L += __shfl_xor(L, d);
-  const auto weight = [&](int i) {
-    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)u32(i < 64 ? f0 : f1), i & 63));
-  };
+  const Weights weight(x0, x1, lane, n);
   float o[C] = {};
 #pragma unroll
   for (int i = 0; i < AHEAD; ++i)
@@ -774,13 +890,7 @@ __global__ void __launch_bounds__(kAttnThreads) kv_attention_join_kernel(AttnArg
 #pragma unroll
       for (int v = 1; v < WAVES; ++v) o[k] += part[v][C * lane + k];
   }
-  const bool empty = M == -__builtin_inff() && L == 0.0f;
-  const float inv = empty ? 0.0f : outer_alpha(a.cache.v_amax[kvh], a.cache.global_fp8_max) / L;
-  const int64_t to = out_row(args, at_, (int)kvh, row);
-  uint16_t* dst = a.out + to * D + C * lane;
-#pragma unroll
-  for (int k = 0; k < C; ++k) dst[k] = empty ? (uint16_t)0 : (uint16_t)bf16_pair(o[k] * inv, 0.0f);
-  if (a.lse && lane == 0) a.lse[to] = empty ? -__builtin_inff() : (M + __builtin_log2f(L)) / kLog2e;
+  put_row<D>(args, at_, kvh, row, lane, o, weight);
 }
 
 // ---------------------------------------------------------------- many rows
@@ -1003,25 +1113,37 @@ AttnPlan kv_attention_plan(const nvfp4_kv_attention_args& a) {
     // Pieces a tile's keys are cut into: the least of a small model of the
     // launch, in microseconds -- rounds of resident workgroups, each with its
     // start and end (C0) and its keys at the speed of a loaded card (V per
-    // workgroup), and the second launch -- over full requests and over
-    // requests of 0.6 of the bound.  Measured at 64 requests of 1024 to 8192
+    // workgroup), and the join: a second launch, or in the first one a memory
+    // latency for every eight pieces of four rows -- over full requests and
+    // over requests of 0.6 of the bound.  Measured at 64 requests of 1024 to 8192
     // keys and 8 heads: 2 pieces 92.8 us, 4 pieces 84.8; 16 requests of up to
-    // 2000: 8 pieces 19.7, 4 pieces 16.4.
+    // 2000: 8 pieces 19.7, 4 pieces 16.4.  Joined in the first launch against a
+    // second one: 4 rows of 1 request over 8191 keys 10.9 us against 12.2, 8
+    // rows of 32 requests over up to 4000 29 against 33, 32 rows of 8 over up
+    // to 8192 34 against 30.
     const double C0 = 5, V = 60.0 * 128 / D;
     const int64_t resident = (int64_t)device_cu_count() * attn_waves(D, p.nq);
     // tiles that an even batch has (p.tiles has room for any)
     const int64_t even = a.tokens * group / p.rows;
     const int64_t likely = (even > a.batch ? even : a.batch) * a.cache.kv_heads;
+    // rows of an average tile, and whether there is a counter for each of the
+    // most tiles; the same with and without cu_q, and whether counters are
+    // given or not, so that the pieces and with them the bits are the same
+    const int64_t joined = rows < p.rows ? rows : p.rows;
+    const bool counters = (even + a.batch + 1) * a.cache.kv_heads <= kJoinCounters;
     double best = 0;
     // past 16 rounds there is nothing left to even out, only workspace to fill
     for (int n = 1; n == 1 || (n <= kMaxSplits && (n - 1) * (int64_t)128 < keys && likely * n <= 16 * resident);
          n += 1 + n / 16) {
       const int64_t all = likely * n;
       const int64_t rounds = (all + resident - 1) / resident + (3 * all + 5 * resident - 1) / (5 * resident);
-      const double cost = (double)rounds * (C0 + (double)keys / (n * V)) + (n > 1 ? 6 + 0.1 * n : 0);
+      const int64_t trips = (joined + 3) / 4 * ((n + 7) / 8);
+      const double second = 6 + 0.1 * n, here = counters ? 3.0 + (double)trips : second;
+      const double cost = (double)rounds * (C0 + (double)keys / (n * V)) + (n == 1 ? 0 : here < second ? here : second);
       if (n == 1 || cost < best) {
         best = cost;
         p.splits = n;
+        p.join = a.counters && n > 1 && here < second;
       }
     }
     p.chunk = (int)((keys + p.splits - 1) / p.splits);
@@ -1044,7 +1166,7 @@ static void launch_dim(const AttnArgs& x, const AttnPlan& p, hipStream_t s) {
   const auto launch = [&](auto nq) {
     constexpr int NQ = decltype(nq)::value;
     hipLaunchKernelGGL((kv_attention_keys_kernel<D, NQ>), grid, block, 0, s, x);
-    if (p.splits == 1) return;
+    if (p.splits == 1 || p.join) return;
     const int64_t tiles = p.tiles * x.a.cache.kv_heads;
     if (p.splits >= kManyPieces)
       hipLaunchKernelGGL((kv_attention_join_kernel<D, 16 * NQ, 4>), dim3((unsigned)(tiles * rows)), block, 0, s, x, rows);
@@ -1067,6 +1189,7 @@ hipError_t launch_kv_attention(const nvfp4_kv_attention_args& a, const AttnPlan&
   if (x.a.window > INT32_MAX) x.a.window = 0;  // reaches past every position
   x.rows = p.rows;
   x.splits = p.splits;
+  x.join = p.join;
   x.chunk = p.chunk;
   x.shift = __builtin_ctz((unsigned)a.cache.page_size);
   x.group = a.q_heads / a.cache.kv_heads;

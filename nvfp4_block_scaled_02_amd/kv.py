@@ -260,13 +260,18 @@ def _capturing():
     return torch.cuda.is_current_stream_capturing()
 
 
-def _cached_workspace(table, dev, nbytes, zeroed):
+def _place(dev):
+    """Whose workspaces a call uses: those of its (device, stream); None under
+    graph capture, where they belong to the graph."""
+    return None if _capturing() else (dev.index, _stream(dev))
+
+
+def _cached_workspace(table, key, dev, nbytes, zeroed):
     """A workspace of at least nbytes whose first `zeroed` bytes were zero
-    before its first use: one per (device, stream), made larger when needed.
-    Under graph capture a new one each call, as it belongs to the graph."""
+    before its first use: one per place, made larger when needed.  Under graph
+    capture a new one each call."""
     if nbytes == 0:
         return None
-    key = None if _capturing() else (dev.index, _stream(dev))
     ws = table.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
@@ -311,7 +316,7 @@ def qk_norm_rope_bwd(dq_out: Optional[torch.Tensor], dk_out: Optional[torch.Tens
             _need(workspace, torch.uint8, "workspace", n)
             ws = workspace
         else:
-            ws = _cached_workspace(_BWD_WORKSPACES, dev, n, n)
+            ws = _cached_workspace(_BWD_WORKSPACES, _place(dev), dev, n, n)
     _invoke("nvfp4_qk_norm_rope_bwd",
             (ctypes.byref(a), _ptr(dq_out), strides[0], _ptr(dk_out), strides[1], _ptr(dws[0]),
              _ptr(dws[1]), _ptr(ws)), dev,
@@ -361,7 +366,8 @@ def kv_read(cache: KVCache, slots: torch.Tensor, *, out: Optional[tuple] = None)
 
 
 # ---------------------------------------------------------------- attention
-_ATTENTION_WORKSPACES = {}
+_ATTENTION_WORKSPACES, _COUNTERS = {}, {}
+KV_COUNTER_BYTES = N.KV_COUNTER_BYTES
 
 
 def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
@@ -369,7 +375,8 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
                  max_seq_len: Optional[int] = None, scale: Optional[float] = None,
                  causal: bool = True, window: int = 0, want_lse: bool = False,
                  out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
-                 workspace: Optional[torch.Tensor] = None):
+                 workspace: Optional[torch.Tensor] = None,
+                 counters: Optional[torch.Tensor] = None):
     """Attention of q [tokens, q_heads, D] over the cache: request b's queries
     are rows cu_q[b] .. cu_q[b+1] (int32; None: one each) and the last of its
     seq_lens[b] tokens (int32), whose pages block_table [batch, width] (int32)
@@ -377,7 +384,10 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
     width); scale: default D^-1/2; window: attend the last `window` tokens only
     (0: all).  Returns out [tokens, q_heads, D] bf16, or (out, lse) with
     want_lse.  workspace: a uint8 tensor of at least the size the library asks
-    for."""
+    for.  counters: a uint8 tensor of KV_COUNTER_BYTES zeros, which every call
+    leaves zero; with it few pieces of a split sequence are joined in the same
+    launch.  Without one a call uses its stream's, and under graph capture none
+    (a graph that is to have them brings its own)."""
     t, h, d, st = _heads(q, "q", None, None, cache.head_dim, 8)
     _check(seq_lens, _I32, "seq_lens")
     batch = seq_lens.numel()
@@ -403,15 +413,21 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
     args = N.KVAttentionArgs(q.data_ptr(), t, st, h, cache._args, block_table.data_ptr(), batch,
                              width, seq_lens.data_ptr(), _ptr(cu_q), max_seq_len,
                              d ** -0.5 if scale is None else scale, int(causal), window,
-                             out.data_ptr(), _ptr(lse), 0)
+                             out.data_ptr(), _ptr(lse), 0, 0)
+    place = _place(dev) if workspace is None or counters is None else None
+    if counters is not None:
+        _check(counters, _U8, "counters", KV_COUNTER_BYTES)
+    elif place is not None:
+        counters = _cached_workspace(_COUNTERS, place, dev, KV_COUNTER_BYTES, KV_COUNTER_BYTES)
+    args.counters = _ptr(counters)
     n = N.lib().nvfp4_kv_attention_workspace_bytes(ctypes.byref(args))
     if workspace is not None:
         _check(workspace, _U8, "workspace")
         if workspace.numel() < n:
             raise ValueError(f"workspace must hold {n} bytes, got {workspace.numel()}")
     else:
-        workspace = _cached_workspace(_ATTENTION_WORKSPACES, dev, n, 0)
+        workspace = _cached_workspace(_ATTENTION_WORKSPACES, place, dev, n, 0)
     args.workspace = _ptr(workspace)
     _invoke("nvfp4_kv_attention", (ctypes.byref(args),), dev,
-            (q, cache, block_table, seq_lens, cu_q, out, lse, workspace, args))
+            (q, cache, block_table, seq_lens, cu_q, out, lse, workspace, counters, args))
     return (out, lse) if lse is not None else out

@@ -179,6 +179,8 @@ static void attention_calls(void) {
               if (bytes && a.tokens) BAD(nvfp4_kv_attention(&a, 0));
               a.workspace = pool;
               OK(nvfp4_kv_attention(&a, 0));
+              a.counters = pool;
+              OK(nvfp4_kv_attention(&a, 0));
             }
   nvfp4_kv_attention_args a;
   memset(&a, 0, sizeof a);

@@ -382,3 +382,32 @@ def test_window_past_every_position():
         runs = [_run(c, qb[:n], [700, 3, 90], new, window=w, check=w == 0) for w in (0, 2**31 - 1, 2**31, 2**63 - 1)]
         for o, l in runs[1:]:
             assert np.array_equal(o, runs[0][0]) and np.array_equal(l, runs[0][1])
+
+
+@pytest.mark.parametrize("d,hq,h,lens,new", [
+    (128, 32, 8, [8191], [1]), (128, 8, 2, [2000, 31, 700, 1999, 1], [1] * 5), (64, 4, 1, [5000], [1]),
+    (192, 6, 2, [3000, 10], [1, 1]), (256, 4, 2, [4000, 0, 129], [1] * 3), (128, 8, 4, [6000, 300], [2, 1])])
+def test_joined_in_the_first_launch_or_a_second(d, hq, h, lens, new):
+    """With counters the pieces of a sequence are joined in the first launch,
+    without (under capture) by a second one: the same bits, and the counters
+    are left zero."""
+    c = _make(lens, 16, h, d, 83)
+    qb = _queries(sum(new), hq, d, 83)
+    want, _ = _run(c, qb, lens, new)
+    cache, q, table = _dev_cache(c), dev_bf16(qb), torch.from_numpy(c["table"]).cuda()
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0] + list(np.cumsum(new)), dtype=torch.int32, device="cuda")
+    counters = torch.zeros(nv.KV_COUNTER_BYTES, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        second = nv.kv_attention(q, cache, table, n, cu)
+        first = nv.kv_attention(q, cache, table, n, cu, counters=counters)
+    for _ in range(3):
+        first.zero_(), second.zero_()
+        g.replay()
+        eager = nv.kv_attention(q, cache, table, n, cu, counters=counters)
+        torch.cuda.synchronize()
+        for o in (first, second, eager):
+            assert np.array_equal(o.float().cpu().numpy().astype(np.float64), want)
+        assert not counters.any()

@@ -188,6 +188,13 @@ def test_attention_rejects(kw):
     assert _attn(**kw) == INV
 
 
+def test_attention_counters_are_aligned_and_change_no_size():
+    assert _attn(counters=FAKE + 8) == INV
+    for kw in (dict(tokens=3, cu_q=None), dict(tokens=3), dict(tokens=6)):
+        a, b = (_attn_args(max_seq_len=100000, counters=c, **kw) for c in (None, FAKE))
+        assert N.lib().nvfp4_kv_attention_workspace_bytes(a) == N.lib().nvfp4_kv_attention_workspace_bytes(b) > 0
+
+
 def test_attention_positions_stay_in_32_bits():
     assert _attn(table_width=(1 << 26) + 1) == UNS
 
