@@ -159,9 +159,9 @@ def kv_plan(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.T
     dev = ctx_lens.device
     if out is None:
         # one allocation: the 32-bit outputs one after another
-        words = torch.empty(2 * batch + tokens + 3, dtype=_I32, device=dev)
+        words = ctx_lens.new_empty(2 * batch + tokens + 3)
         cu, lens, pos, count, refused = words.split((batch + 1, batch, tokens, 1, 1))
-        out = KVPlan(cu, lens, pos, torch.empty(tokens, dtype=_I64, device=dev), count, refused)
+        out = KVPlan(cu, lens, pos, ctx_lens.new_empty(tokens, dtype=_I64), count, refused)
     else:
         _check(out.cu_new, _I32, "cu_new", batch + 1)
         _check(out.seq_lens, _I32, "seq_lens", batch)
@@ -206,7 +206,7 @@ def _out_of(x, given, n):
     if x is None:
         return None, 0, 0
     if given is None:
-        given = torch.empty(x.shape, dtype=_BF16, device=x.device)
+        given = x.new_empty(x.shape)
         return given, given.data_ptr(), x.shape[1] * x.shape[2]
     return given, given.data_ptr(), _heads(given, n + "_out", *x.shape)[3]
 
@@ -305,7 +305,7 @@ def qk_norm_rope_bwd(dq_out: Optional[torch.Tensor], dk_out: Optional[torch.Tens
         if w is not None:
             dw = out.get(f"d{n}_weight")
             if dw is None:
-                dw = torch.empty(a.head_dim, dtype=_F32, device=dev)
+                dw = w.new_empty(a.head_dim, dtype=_F32)
             else:
                 _check(dw, _F32, f"d{n}_weight", a.head_dim)
         dws.append(dw)
@@ -355,8 +355,7 @@ def kv_read(cache: KVCache, slots: torch.Tensor, *, out: Optional[tuple] = None)
     n = slots.numel()
     h, d = cache.kv_heads, cache.head_dim
     if out is None:
-        out = (torch.empty((n, h, d), dtype=_BF16, device=slots.device),
-               torch.empty((n, h, d), dtype=_BF16, device=slots.device))
+        out = tuple(slots.new_empty((2, n, h, d), dtype=_BF16).unbind(0))
     else:
         for o, name in zip(out, ("k_out", "v_out")):
             _check(o, _BF16, name, n * h * d)
@@ -400,7 +399,7 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
         raise ValueError(f"without cu_q every request has one query: {t} rows, {batch} requests")
     dev = q.device
     if out is None:
-        out = torch.empty((t, h, d), dtype=_BF16, device=dev)
+        out = q.new_empty((t, h, d))
     else:
         _check(out, _BF16, "out", t * h * d)
     if lse is None and want_lse:
