@@ -1111,35 +1111,51 @@ AttnPlan kv_attention_plan(const nvfp4_kv_attention_args& a) {
   p.chunk = 0x7FFFFF80;
   if (!p.rows_split && keys > 128) {
     // Pieces a tile's keys are cut into: the least of a small model of the
-    // launch, in microseconds -- rounds of resident workgroups, each with its
-    // start and end (C0) and its keys at the speed of a loaded card (V per
-    // workgroup), and the join: a second launch, or in the first one a memory
-    // latency for every eight pieces of four rows -- over full requests and
-    // over requests of 0.6 of the bound.  Measured at 64 requests of 1024 to 8192
-    // keys and 8 heads: 2 pieces 92.8 us, 4 pieces 84.8; 16 requests of up to
-    // 2000: 8 pieces 19.7, 4 pieces 16.4.  Joined in the first launch against a
-    // second one: 4 rows of 1 request over 8191 keys 10.9 us against 12.2, 8
-    // rows of 32 requests over up to 4000 29 against 33, 32 rows of 8 over up
-    // to 8192 34 against 30.
-    const double C0 = 5, V = 60.0 * 128 / D;
-    const int64_t resident = (int64_t)device_cu_count() * attn_waves(D, p.nq);
+    // launch, in microseconds, over full requests and over requests of part of
+    // the bound; the join is a second launch, or in the first one a memory
+    // latency for every eight pieces of four rows.
+    // 16 rows a wavefront: the keys come at the speed of the card (CARD a CU)
+    // or, where the pieces are spread unevenly, at that of the CU with the most
+    // of them (WG); each piece a CU takes costs its start and end; of uneven
+    // requests part of the longest piece runs alone.  Fitted to 17 shapes timed
+    // with 1 to 96 pieces, e.g. 64 requests of 8191 keys and 8 heads: 1 piece
+    // 113 us, 2 120, 5 122; 32 of up to 8000: 1 piece 53, 2 44, 6 48; 4 of
+    // 32000: 8 pieces 31, 16 33; 16 of up to 2000: 1 piece 16.8, 4 13.5, 8 17.4.
+    // More rows: bound by their arithmetic, so rounds of resident workgroups,
+    // each with its start and end and its keys (70 us for 3 requests of 4 drafted
+    // tokens over up to 131072 where the model above takes 73 to 85).
+    // Joined in the first launch against a second one: 4 rows of 1 request over
+    // 8191 keys 10.8 us against 11.5, 8 rows of 32 over up to 4000 28.0 against
+    // 30.4, 32 rows of 8 over up to 8192 33.3 against 28.9.
+    const double cus = device_cu_count(), resident = cus * attn_waves(D, p.nq);
+    const double CARD = 140.0 * 128 / D, WG = (p.nq > 1 ? 60.0 : 200.0) * 128 / D;
     // tiles that an even batch has (p.tiles has room for any)
     const int64_t even = a.tokens * group / p.rows;
-    const int64_t likely = (even > a.batch ? even : a.batch) * a.cache.kv_heads;
+    const double likely = (double)((even > a.batch ? even : a.batch) * a.cache.kv_heads);
     // rows of an average tile, and whether there is a counter for each of the
     // most tiles; the same with and without cu_q, and whether counters are
     // given or not, so that the pieces and with them the bits are the same
     const int64_t joined = rows < p.rows ? rows : p.rows;
     const bool counters = (even + a.batch + 1) * a.cache.kv_heads <= kJoinCounters;
     double best = 0;
-    // past 16 rounds there is nothing left to even out, only workspace to fill
-    for (int n = 1; n == 1 || (n <= kMaxSplits && (n - 1) * (int64_t)128 < keys && likely * n <= 16 * resident);
-         n += 1 + n / 16) {
-      const int64_t all = likely * n;
-      const int64_t rounds = (all + resident - 1) / resident + (3 * all + 5 * resident - 1) / (5 * resident);
+    // past 64 pieces a CU there is nothing left to even out, only workspace to fill
+    for (int n = 1; n == 1 || (n <= kMaxSplits && (n - 1) * (int64_t)128 < keys && likely * n <= 64 * cus); ++n) {
+      const int64_t each = ((keys + n - 1) / n + 127) & ~(int64_t)127;
+      if (n > 1 && (keys + each - 1) / each != n) continue;  // as fewer pieces
+      const double piece = (double)(each < keys ? each : keys) / WG;
+      double cost;
+      if (p.nq > 1) {
+        cost = (ceil(likely * n / resident) + ceil(0.6 * likely * n / resident)) * (5 + piece);
+      } else {
+        const double all = likely * (double)keys / (cus * CARD);
+        const double most = ceil(likely * n / cus), some = likely * (n * 0.7 > 1 ? n * 0.7 : 1) / cus;
+        const double fewer = some > 1 ? some : 1;
+        cost = (all > most * piece ? all : most * piece) + 4 * most +
+               (0.7 * all > fewer * piece ? 0.7 * all : fewer * piece) + 4 * fewer + 0.6 * piece;
+      }
       const int64_t trips = (joined + 3) / 4 * ((n + 7) / 8);
-      const double second = 6 + 0.1 * n, here = counters ? 3.0 + (double)trips : second;
-      const double cost = (double)rounds * (C0 + (double)keys / (n * V)) + (n == 1 ? 0 : here < second ? here : second);
+      const double second = 7 + 0.1 * n, here = counters ? 3 + 1.5 * (double)trips : second;
+      cost += n == 1 ? 0 : here < second ? here : second;
       if (n == 1 || cost < best) {
         best = cost;
         p.splits = n;
