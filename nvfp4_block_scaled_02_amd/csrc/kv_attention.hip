@@ -30,13 +30,12 @@
 // wavefront has rows of its own, and the workgroup dequantizes each block of
 // keys once, into LDS.
 //
-// Measured with 32 query and 8 key heads of 128 values: 64 requests of up to
-// 8192 keys 77 .. 84 us (341 MB of cache, 66 us at the rate of a copy; 64 even
-// ones of 32768 keys run at 5.4 TB/s; vector units 69 % busy, matrix units
-// 15), one of 8191 keys 11.7; 2 x 2048 tokens behind 6000 cached ones 356 ..
-// 378 us, 840 to 890 TFLOP/s (263 us at the rate of a large product; vector
-// units 56 % busy with softmax and dequantization, matrix units 41), a prompt
-// of 8191 tokens 601 us.
+// Measured with 32 query and 8 key heads of 128 values: 64 requests of 8191
+// keys 115 us (5.3 TB/s, the rate of a copy), of up to 8192 78 .. 84 (341 MB,
+// 66 us at that rate; vector units 59 % busy, matrix units 16), one of 8191
+// keys 10.7; 2 x 2048 tokens behind 6000 cached ones 355 .. 361 us, 880 to 900
+// TFLOP/s (263 us at the rate of a large product; vector units 55 % busy with
+// softmax and dequantization, matrix units 41), a prompt of 8191 tokens 582.
 #include <math.h>
 
 #include "kv.hpp"

@@ -9,7 +9,7 @@ namespace nvfp4 {
 // flight while one is computed.  Each value is read and written once: 8192
 // tokens of 32 + 8 heads of 128 values move 172 MB in 30 us (5.7 TB/s, partly
 // from the last-level cache; a copy of the query view alone by the library
-// takes 28).  The arithmetic in 64 bits keeps the vector units 80 % busy.
+// takes 28).  The arithmetic in 64 bits keeps the vector units 77 % busy.
 template <int LPH, int PAIRS>
 __global__ void __launch_bounds__(kRowThreads)
 qk_norm_rope_kernel(nvfp4_qk_args a, RowGrid grid) {
@@ -138,8 +138,8 @@ __device__ __forceinline__ double sum_slots(const double* slots, int n, int e, i
 // atomic addition, the same bits on every run.  Slots are written and read at
 // the level that the whole GPU sees, so no cache is written back.
 // Bound by its bytes: 261 MB (254 without the partial sums) in 50 us at 8192
-// tokens of 32 + 8 heads of 128, 5.2 TB/s with the vector units 74 % busy;
-// 1023 tokens of 12 + 4 heads of 64 take 12.8 us, most of it latency.
+// tokens of 32 + 8 heads of 128, 5.2 TB/s with the vector units 71 % busy;
+// 1023 tokens of 12 + 4 heads of 64 take 12.3 us, most of it latency.
 template <int LPH, int PAIRS>
 __global__ void __launch_bounds__(kRowThreads, 4)
 qk_norm_rope_bwd_kernel(BwdArgs b) {
