@@ -1116,8 +1116,9 @@ AttnPlan kv_attention_plan(const nvfp4_kv_attention_args& a) {
     // 16 rows a wavefront: the keys come at the speed of the card (CARD a CU)
     // or, where the pieces are spread unevenly, at that of the CU with the most
     // of them (WG); each piece a CU takes costs its start and end; of uneven
-    // requests part of the longest piece runs alone.  Fitted to 17 shapes timed
-    // with 1 to 96 pieces, e.g. 64 requests of 8191 keys and 8 heads: 1 piece
+    // requests part of the longest piece runs alone.  Fitted to 28 shapes timed
+    // with 1 to 96 pieces (3 % over the best of them on average; at most
+    // 25 %, 2 tokens each of 32 requests of 3000 keys), e.g. 64 requests of 8191 keys and 8 heads: 1 piece
     // 113 us, 2 120, 5 122; 32 of up to 8000: 1 piece 53, 2 44, 6 48; 4 of
     // 32000: 8 pieces 31, 16 33; 16 of up to 2000: 1 piece 16.8, 4 13.5, 8 17.4.
     // More rows: bound by their arithmetic, so rounds of resident workgroups,
@@ -1147,13 +1148,13 @@ AttnPlan kv_attention_plan(const nvfp4_kv_attention_args& a) {
         cost = (ceil(likely * n / resident) + ceil(0.6 * likely * n / resident)) * (5 + piece);
       } else {
         const double all = likely * (double)keys / (cus * CARD);
-        const double most = ceil(likely * n / cus), some = likely * (n * 0.7 > 1 ? n * 0.7 : 1) / cus;
+        const double most = ceil(likely * n / cus), some = likely * (n * 0.8 > 1 ? n * 0.8 : 1) / cus;
         const double fewer = some > 1 ? some : 1;
-        cost = (all > most * piece ? all : most * piece) + 4 * most +
-               (0.7 * all > fewer * piece ? 0.7 * all : fewer * piece) + 4 * fewer + 0.6 * piece;
+        cost = (all > most * piece ? all : most * piece) + 3 * most +
+               (0.8 * all > fewer * piece ? 0.8 * all : fewer * piece) + 3 * fewer + 0.6 * piece;
       }
       const int64_t trips = (joined + 3) / 4 * ((n + 7) / 8);
-      const double second = 7 + 0.1 * n, here = counters ? 3 + 1.5 * (double)trips : second;
+      const double second = 7 + 0.1 * n, here = counters ? 2 + 1.5 * (double)trips : second;
       cost += n == 1 ? 0 : here < second ? here : second;
       if (n == 1 || cost < best) {
         best = cost;
