@@ -63,7 +63,7 @@ static nvfp4_qk_args qk_of(int64_t tokens, int hq, int hk, int d, int rot) {
   a.k_stride = a.k_out_stride = (int64_t)hk * d;
   a.positions = P(const int32_t, 2560);
   a.cos = P(const float, 2816);
-  a.sin = P(const float, 3072);
+  a.sin = P(const float, 4352);
   a.max_pos = 1000;
   a.rot_dim = rot;
   a.q_weight = P(const uint16_t, 3328);
