@@ -76,9 +76,10 @@ struct BwdArgs {
   RowGrid grid;
 };
 
-// One head's gradient in the lane; g n is added to dw.
+// One head's gradient in the lane; g n is added to dw.  A lane that is not on
+// holds zeros, and its r is 0 (not 0^-1/2, where eps is 0): it adds nothing.
 template <int LPH, int PAIRS>
-__device__ __forceinline__ Row8 row_bwd(const Row8& in, const Row8& grad, const RowMap<LPH>& m, bool norm,
+__device__ __forceinline__ Row8 row_bwd(const Row8& in, const Row8& grad, const RowMap<LPH>& m, bool on, bool norm,
                                         const Row8& weight, float eps, float inv_d,
                                         const RowAngles& ang, float (&dw)[8]) {
   float g[8];
@@ -91,7 +92,7 @@ __device__ __forceinline__ Row8 row_bwd(const Row8& in, const Row8& grad, const 
 #pragma unroll
     for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(x[i], x[i], ss);
     const float v = row_sum<LPH>(ss) * inv_d + eps;
-    const float r = __builtin_isinf(v) ? 0.0f : 1.0f / __builtin_sqrtf(v);
+    const float r = !on || __builtin_isinf(v) ? 0.0f : 1.0f / __builtin_sqrtf(v);
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -180,7 +181,8 @@ qk_norm_rope_bwd_kernel(BwdArgs b) {
         const Row8 xn = load(x, gn), yn = load(y, gn);
         // lanes without values, and heads past the last one, add nothing
         const bool on = m.active && head_of(g) < heads;
-        const Row8 r = row_bwd<LPH, PAIRS>(xv.or_zero(on), yv.or_zero(on), m, norm, weight, eps, inv_d, ang, dw);
+        const Row8 r = row_bwd<LPH, PAIRS>(xv.or_zero(on), yv.or_zero(on), m, on, norm, weight, eps, inv_d, ang,
+                                               dw);
         if (on) row_store(d + head_of(g) * D, m, r);
         xv = xn;
         yv = yn;
