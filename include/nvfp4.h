@@ -613,8 +613,8 @@ int nvfp4_qk_norm_rope(const nvfp4_qk_args* args, hipStream_t stream);
  * nvfp4_qk_norm_rope_bwd -- its gradient.  With g = the incoming gradient
  * rotated back, n = x * r and r = (mean(x^2) + eps)^-1/2:
  *   dx = r * (g w - n * mean(g w n)),  dw = sum over tokens and heads of g n
- * (w NULL: dx = g, no dw), in binary32, dw's sums in binary64 in a fixed
- * order.  At eps = 0 a head of zeros is 0 / 0: NaN in its dx and in dw.
+ * (w NULL: dx = g, no dw), in binary32 (r of heads whose squares leave it in
+ * binary64), dw's sums in binary64 in a fixed order.  At eps = 0 a head of zeros is 0 / 0: NaN in its dx and in dw.
  * args->q, k and the tables as in the forward call; args->q_out and
  * k_out with their strides are the OUTPUTS dq and dk (bf16); dq_out, dk_out
  * the incoming gradients (bf16) with strides gq_stride and gk_stride.

@@ -92,7 +92,23 @@ __device__ __forceinline__ Row8 row_bwd(const Row8& in, const Row8& grad, const 
 #pragma unroll
     for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(x[i], x[i], ss);
     const float v = row_sum<LPH>(ss) * inv_d + eps;
-    const float r = !on || __builtin_isinf(v) ? 0.0f : 1.0f / __builtin_sqrtf(v);
+    float r = on ? 1.0f / __builtin_sqrtf(v) : 0.0f;
+    // r = r 2^up of a head whose squares leave binary32 (a bf16 value's do
+    // beyond 2^64 and below 2^-75): from binary64, as in the forward call
+    int up = 0;
+    const bool far = on && !(v > 0x1p-100f && v < 0x1p100f), any_far = __any(far);
+    if (any_far) {
+      double ss64 = 0.0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss64 = __builtin_fma((double)x[i], (double)x[i], ss64);
+      const double r64 = rsqrt64(row_sum<LPH>(ss64) * (double)inv_d + (double)eps);
+      if (far) {
+        r = (float)__builtin_amdgcn_frexp_mant(r64);
+        up = __builtin_amdgcn_frexp_exp(r64);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __builtin_ldexpf(x[i], up);
+      }
+    }
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -104,6 +120,10 @@ __device__ __forceinline__ Row8 row_bwd(const Row8& in, const Row8& grad, const 
     dot = row_sum<LPH>(dot) * inv_d;
 #pragma unroll
     for (int i = 0; i < 8; ++i) g[i] = r * __builtin_fmaf(-x[i], dot, g[i]);
+    if (any_far) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) g[i] = __builtin_ldexpf(g[i], up);
+    }
   }
   return Row8{make_uint2(bf16_pair(g[0], g[1]), bf16_pair(g[2], g[3])),
               make_uint2(bf16_pair(g[4], g[5]), bf16_pair(g[6], g[7]))};

@@ -55,3 +55,21 @@ def test_no_eps_and_a_row_of_zeros():
     _bwd_close(dq[~bad], want[0][0][~bad], want[0][2][~bad], 64, "the other rows")
     assert torch.isnan(got[2]).all()
     _weights_close(got[3], want[1][1], want[1][3], 64, "the keys' side")
+
+
+@pytest.mark.parametrize("d,hq,hk", [(64, 3, 2), (128, 4, 1), (192, 2, 3), (256, 5, 2)])
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+def test_rows_whose_squares_leave_binary32(d, hq, hk, eps):
+    """The forward call norms rows of any size, and so does its gradient:
+    magnitudes from 2^-110 to 2^110 beside ordinary ones."""
+    t = 40
+    x, w, pos, cos, sin = _inputs(t, hq, hk, d, d, d)
+    rng = np.random.default_rng(d)
+    for i in range(2):
+        e = rng.choice([-110, -70, -58, 0, 0, 45, 58, 70, 110], (t, x[i].shape[1], 1))
+        x[i] = R.bits(rng.standard_normal(x[i].shape) * 2.0 ** e)
+    got, want = _gradient(x, w, pos, cos, sin, eps, d)
+    for i, (dx, dw, mag, wmag) in enumerate(want):
+        assert (np.abs(dx) < 3e38).all() and np.abs(dx).max(-1).min() > 0
+        _bwd_close(_bits_of(got[i]), dx, mag, d, ("dx", i))
+        _weights_close(got[2 + i], dw, wmag, d, ("dw", i))
