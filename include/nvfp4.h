@@ -685,8 +685,11 @@ int nvfp4_kv_read(const nvfp4_kv_cache* cache, const int64_t* slots, int64_t tok
  * Products of codes and block scales are exact in binary16; q is scaled by a
  * power of two per row and held in binary16 (exact for values within 2^-14 of
  * the row's largest, and nearer than 2^-25 of it below); scores, maxima, sums
- * and outputs accumulate in binary32, the softmax weights round once to
- * binary16 (relative 2^-11).
+ * and outputs accumulate in binary32 (scores past 10^8 in magnitude, which it
+ * no longer tells apart, may give NaN).  The softmax weights round once to
+ * binary16, in the output's sums and in lse alike: each by 2^-11 of itself or
+ * by 2^-32 of the row's largest, whichever is more, so that n keys far below
+ * one large score may lose up to n 2^-32 of the row's sum.
  *   q         bf16 [tokens, q_heads, D], heads dense, q_stride from token to
  *             token (a multiple of 8), 16-byte aligned.
  *   out       bf16 [tokens, q_heads, D] dense, 16-byte aligned.

@@ -14,10 +14,11 @@
 //   S^T = K Q^T   two 16 x 16 products over D: lane (r, g) reads key 8 (r/4) +
 //     4 t + r % 4 and its values [g D/4, (g+1) D/4): whole 16-byte loads, and
 //     lane (n, g) receives the scores of query n with keys 8 g + 4 t + 0..3
-//   softmax       per lane, in the exponent of 2: the running maximum moves
-//     only when a score passes it by more than 2^8 (weights stay below 2^8,
-//     far inside binary16), so a tile usually needs no exchange between lanes
-//     and no rescaling; the weights' sum is one more product, with ones
+//   softmax       per lane, in the exponent of 2: weights are 2^(s - m) with m
+//     set kLift below the largest score so far, and m moves only when a score
+//     passes it by more than 15 (weights stay within binary16's 2^15), so a tile
+//     usually needs no exchange between lanes and no rescaling; the weights'
+//     sum is one more product, with ones
 //   O^T += V^T P^T  lane (m, g) reads keys 8 g .. 8 g + 7 of 4 value columns
 //     as the cache holds them (8 tokens side by side); lane (n, g)'s weights
 //     of keys 8 g .. 8 g + 7 are already the product's other operand.
@@ -51,6 +52,11 @@ constexpr int kManyPieces = 16;
 constexpr int kJoinCounters = NVFP4_KV_COUNTER_BYTES / 128;
 constexpr int kSlabStride = 68;  // floats of a 64-column slab row: 4 apart in the banks
 constexpr float kLog2e = 1.44269504088896340736f;
+// The largest weight of a row is 2^kLift and more: what binary16 rounds to 0
+// is below 2^-(25 + kLift) of it.  The rest up to 2^15 is how far the scores
+// may climb before a tile rescales its sums (11 and 4 instead of 7 and 8 take
+// 0.6 % longer in prompt chunks).
+constexpr float kLift = 7.0f;
 
 struct AttnArgs {
   nvfp4_kv_attention_args a;
@@ -306,7 +312,8 @@ struct Walk {
   f16x8 q[NQ][NCH];
   f32x4 o[NQ][NJ][4];  // [j][e][i]: query n, column 64 j + 16 g + 4 i + e
   float factor[NQ];    // binary32 factor of a row's scores
-  float m[NQ], thr[NQ];
+  float m[NQ];         // exponent that the row's weights and sums are scaled by
+  float thr[NQ];       // largest score that m may stay for
   f32x4 l[NQ];         // sum of a row's weights, four times
   int lo[NQ], hi[NQ];  // keys that the row attends
 
@@ -365,10 +372,10 @@ struct Walk {
   __device__ __forceinline__ float top_of(int n, const f32x4& s0, const f32x4& s1) const {
     return factor[n] * max3(max3(s0[0], s0[1], s0[2]), max3(s0[3], s1[0], s1[1]), max3(s1[2], s1[3], s1[3]));
   }
-  // Moves the maxima of all rows where a score passes one by 2^8.  A NaN score
-  // never does; its weight and the row become NaN.  One branch for all rows,
-  // so that what surrounds it stays in long runs that the matrix and the
-  // vector units share.
+  // Moves the exponents of all rows where a score passes one by more than 15.
+  // A NaN score never does; its weight and the row become NaN.  One branch for
+  // all rows, so that what surrounds it stays in long runs that the matrix and
+  // the vector units share.
   __device__ __forceinline__ void raise(const float (&top)[NQ]) {
     bool passed = false;
 #pragma unroll
@@ -377,8 +384,10 @@ struct Walk {
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
       const float was = m[n];
-      m[n] = __builtin_fmaxf(m[n], max_over_g(top[n]));
-      thr[n] = m[n] + 8.0f;
+      m[n] = __builtin_fmaxf(m[n], max_over_g(top[n]) - kLift);
+      // less by a step of m, so that where scores past 2^20 make steps of an
+      // eighth and more, no sum rounds up past 15
+      thr[n] = m[n] + __builtin_fmaf(__builtin_fabsf(m[n]), -0x1p-23f, 15.0f);
       const float keep = was == m[n] || was == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(was - m[n]);
       l[n] *= keep;
 #pragma unroll
