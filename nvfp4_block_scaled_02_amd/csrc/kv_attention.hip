@@ -434,7 +434,11 @@ struct Walk {
   // ... and in binary16, each row scaled by a power of two.
   __device__ __forceinline__ void start(const AttnArgs& args, int kvh, const RawQ& raw) {
     const nvfp4_kv_attention_args& a = args.a;
-    const float common = outer_alpha(a.cache.k_amax[kvh], a.cache.global_fp8_max) * __builtin_fabsf(a.scale) * kLog2e;
+    float common = outer_alpha(a.cache.k_amax[kvh], a.cache.global_fp8_max) * __builtin_fabsf(a.scale) * kLog2e;
+    // An unusable amax makes the queries NaN, not the factor: a score that a
+    // mask has replaced by -infinity is multiplied by the factor too.
+    const bool unusable = common != common;
+    common = unusable ? 1.0f : common;
 #pragma unroll
     for (int n = 0; n < NQ; ++n) {
       uint32_t top = 0;
@@ -450,7 +454,7 @@ struct Walk {
       int e = 254 - (int)(u32(topf) >> 23);  // exponent field of 2^-floor(log2 top)
       e = topf == 0.0f ? 127 : e < 1 ? 1 : e > 254 ? 254 : e;
       // a negative scale turns the row's sign, so that factor >= 0
-      const float up = __builtin_copysignf(__uint_as_float((uint32_t)e << 23), a.scale);
+      const float up = unusable ? __builtin_nanf("") : __builtin_copysignf(__uint_as_float((uint32_t)e << 23), a.scale);
 #pragma unroll
       for (int i = 0; i < NCH; ++i) {
         const uint32_t x[4] = {raw.x[n][i].x, raw.x[n][i].y, raw.x[n][i].z, raw.x[n][i].w};

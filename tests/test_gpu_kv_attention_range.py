@@ -49,3 +49,16 @@ def test_one_large_score_over_a_long_flat_tail(d, gap, form):
     l = lse.cpu().numpy().astype(np.float64)
     tol = (mass + rel) / (1 + tail) + 4 * R.F32 * np.abs(want_lse)
     assert (np.abs(l - want_lse[:, None]) <= tol[:, None]).all()
+
+
+@pytest.mark.parametrize("amax", [np.nan, np.inf, -1.0])
+@pytest.mark.parametrize("lens,new", [([2, 9], [4, 3]), ([50, 40], [130, 33])])
+def test_rows_that_attend_nothing_under_an_unusable_amax(lens, new, amax):
+    """A key amax that is no amax makes NaN of the rows that attend a key, and
+    of no others: queries before the first token still give 0 and -inf."""
+    c = _make(lens, 8, 2, 64, 32)
+    c["amax"][0][0] = amax
+    o, l = _run(c, _queries(sum(new), 4, 64, 32), lens, new)
+    none = new[0] - lens[0]
+    assert (o[:none] == 0).all() and np.isneginf(l[:none]).all()
+    assert np.isnan(o[none:, :2]).all() and np.isfinite(o[none:, 2:]).all()
