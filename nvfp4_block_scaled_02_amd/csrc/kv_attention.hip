@@ -448,13 +448,15 @@ struct Walk {
         top = top > t ? top : t;
       }
       // the row's largest magnitude: bf16 patterns order like their values
-      float topf = __uint_as_float(top << 16);
-      topf = top >= 0x7F80u ? 1.0f : topf;  // infinities and NaN travel as they are
-      topf = max_over_g(topf);
+      // (infinity for a NaN too)
+      const float topf = max_over_g(__uint_as_float((top < 0x7F80u ? top : 0x7F80u) << 16));
       int e = 254 - (int)(u32(topf) >> 23);  // exponent field of 2^-floor(log2 top)
       e = topf == 0.0f ? 127 : e < 1 ? 1 : e > 254 ? 254 : e;
+      // Against an infinite value every key's score is infinite or NaN, and a
+      // softmax of infinities of either sign is NaN: so is the row, then.
+      const bool nan = unusable || topf == __builtin_inff();
       // a negative scale turns the row's sign, so that factor >= 0
-      const float up = unusable ? __builtin_nanf("") : __builtin_copysignf(__uint_as_float((uint32_t)e << 23), a.scale);
+      const float up = nan ? __builtin_nanf("") : __builtin_copysignf(__uint_as_float((uint32_t)e << 23), a.scale);
 #pragma unroll
       for (int i = 0; i < NCH; ++i) {
         const uint32_t x[4] = {raw.x[n][i].x, raw.x[n][i].y, raw.x[n][i].z, raw.x[n][i].w};

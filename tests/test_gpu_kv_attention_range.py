@@ -62,3 +62,19 @@ def test_rows_that_attend_nothing_under_an_unusable_amax(lens, new, amax):
     none = new[0] - lens[0]
     assert (o[:none] == 0).all() and np.isneginf(l[:none]).all()
     assert np.isnan(o[none:, :2]).all() and np.isfinite(o[none:, 2:]).all()
+
+
+@pytest.mark.parametrize("lens,new", [([1, 5, 40, 40], [1, 1, 1, 2]), ([150], [140])])
+@pytest.mark.parametrize("x", [0x7F80, 0xFF80])
+def test_infinite_queries_against_keys_of_one_sign(lens, new, x):
+    """exp(-inf + inf) is no number: a row whose scores are all infinite is NaN
+    whatever their sign, unlike a row that attends nothing."""
+    c = _make(lens, 16, 1, 128, 33)
+    used = c["ks"][..., :1] != 0x7F
+    c["kc"][..., :1] = np.where(used, (c["kc"][..., :1] & 0xF0) | 3, c["kc"][..., :1])  # value 0: +1.5 everywhere
+    qb = _queries(sum(new), 2, 128, 33)
+    qb[:, 0, 0] = x
+    for scale in (0.1, -0.1):
+        o, l = _run(c, qb, lens, new, scale=scale)
+        assert np.isnan(o[:, 0]).all() and np.isnan(l[:, 0]).all()
+        assert np.isfinite(o[:, 1]).all() and np.isfinite(l[:, 1]).all()
