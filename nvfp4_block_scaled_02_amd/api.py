@@ -119,13 +119,22 @@ class Launch:
             N.check(st, self._entry)
 
 
-_CAPTURE = threading.local()
+class _Capture(threading.local):
+    launches = None  # the list that prepare() collects, inside it
+
+
+_CAPTURE = _Capture()
+
+
+def _preparing() -> bool:
+    """Inside prepare(): the call becomes a Launch, which runs on any stream."""
+    return _CAPTURE.launches is not None
 
 
 def _invoke(entry: str, args: tuple, device, keep):
     """Issues entry(*args, stream) on the current stream of `device` now, or,
     inside prepare(), records it as a Launch instead."""
-    rec = getattr(_CAPTURE, "launches", None)
+    rec = _CAPTURE.launches
     if rec is not None:
         rec.append(Launch(entry, args, device, keep))
         return
@@ -138,8 +147,10 @@ def prepare(fn, *args, **kwargs):
     """Runs fn(*args, **kwargs) -- a call of this module that issues exactly
     one library call -- with its arguments checked and its outputs allocated,
     but without launching.  Returns (launch, result): calling `launch()`
-    issues the call, writing the outputs in `result`."""
-    prev = getattr(_CAPTURE, "launches", None)
+    issues the call, writing the outputs in `result`.  Buffers are allocated
+    and zeroed on the stream that is current here: a launch on another one
+    waits for it first, as for any tensor."""
+    prev = _CAPTURE.launches
     _CAPTURE.launches = []
     try:
         result = fn(*args, **kwargs)

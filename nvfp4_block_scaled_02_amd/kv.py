@@ -16,7 +16,7 @@ from typing import Optional
 import torch
 
 from . import _native as N
-from .api import _invoke, _need, _SELECT, _stream, default_global_max
+from .api import _invoke, _need, _preparing, _SELECT, _stream, default_global_max
 
 _PAIRS = {"halves": N.PAIRS_HALVES, "neighbours": N.PAIRS_NEIGHBOURS}
 
@@ -261,15 +261,16 @@ def _capturing():
 
 
 def _place(dev):
-    """Whose workspaces a call uses: those of its (device, stream); None under
-    graph capture, where they belong to the graph."""
-    return None if _capturing() else (dev.index, _stream(dev))
+    """Whose workspaces a call uses: those of its (device, stream); None where
+    it gets new ones: under graph capture (the graph's) and inside prepare()
+    (the Launch's, which may run on any stream, beside any other call)."""
+    return None if _preparing() or _capturing() else (dev.index, _stream(dev))
 
 
 def _cached_workspace(table, key, dev, nbytes, zeroed):
     """A workspace of at least nbytes whose first `zeroed` bytes were zero
-    before its first use: one per place, made larger when needed.  Under graph
-    capture a new one each call."""
+    before its first use: one per place, made larger when needed; a new one
+    each call without a place."""
     if nbytes == 0:
         return None
     ws = table.get(key)
@@ -291,7 +292,10 @@ def qk_norm_rope_bwd(dq_out: Optional[torch.Tensor], dk_out: Optional[torch.Tens
                      workspace: Optional[torch.Tensor] = None):
     """Gradient of qk_norm_rope at (q, k) for the gradients dq_out and dk_out
     of its results: (dq, dk, dq_weight, dk_weight), the last two float32 [D]
-    or None.  out: optional {"dq", "dk", "dq_weight", "dk_weight"}."""
+    or None.  out: optional {"dq", "dk", "dq_weight", "dk_weight"}.
+    workspace: a uint8 tensor of the size the library asks for, zeroed before
+    its first use; without one a call uses its stream's, a prepared Launch its
+    own (for runs that do not overlap)."""
     out = out or {}
     a, dq, dk = _qk(q, k, positions, cos, sin, q_weight, k_weight, eps, pairs, out.get("dq"),
                     out.get("dk"))
@@ -385,8 +389,9 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
     want_lse.  workspace: a uint8 tensor of at least the size the library asks
     for.  counters: a uint8 tensor of KV_COUNTER_BYTES zeros, which every call
     leaves zero; with it few pieces of a split sequence are joined in the same
-    launch.  Without one a call uses its stream's, and under graph capture none
-    (a graph that is to have them brings its own)."""
+    launch.  Without them a call uses its stream's (a prepared Launch its own,
+    for runs that do not overlap), and under graph capture a new workspace and
+    no counters (a graph that is to have them brings its own)."""
     t, h, d, st = _heads(q, "q", None, None, cache.head_dim, 8)
     _check(seq_lens, _I32, "seq_lens")
     batch = seq_lens.numel()
@@ -416,7 +421,7 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
     place = _place(dev) if workspace is None or counters is None else None
     if counters is not None:
         _check(counters, _U8, "counters", KV_COUNTER_BYTES)
-    elif place is not None:
+    elif place is not None or not _capturing():
         counters = _cached_workspace(_COUNTERS, place, dev, KV_COUNTER_BYTES, KV_COUNTER_BYTES)
     args.counters = _ptr(counters)
     n = N.lib().nvfp4_kv_attention_workspace_bytes(ctypes.byref(args))

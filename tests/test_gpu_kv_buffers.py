@@ -1,0 +1,51 @@
+"""Whose memory the key/value-cache calls use."""
+import pytest
+
+from helpers import dev_bf16
+from test_gpu_kv_attention import _dev_cache, _make, _queries
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+nv = pytest.importorskip("nvfp4_block_scaled_02_amd")
+
+
+def _split_call(seed=41):
+    """Arguments of an attention call whose keys are cut into pieces."""
+    lens = [3000, 20]
+    c = _make(lens, 16, 2, 128, seed)
+    return (dev_bf16(_queries(2, 8, 128, seed)), _dev_cache(c), torch.from_numpy(c["table"]).cuda(),
+            torch.tensor(lens, dtype=torch.int32, device="cuda"))
+
+
+def _struct(launch):
+    return launch._args[0]._obj
+
+
+def test_prepared_attentions_have_buffers_of_their_own():
+    args = _split_call()
+    want = nv.kv_attention(*args)  # the stream's own buffers exist
+    launches = [nv.prepare(nv.kv_attention, *args) for _ in range(2)]
+    for field in ("workspace", "counters"):
+        own = [getattr(_struct(l), field) for l, _ in launches]
+        shared = [t.data_ptr() for t in (*nv.kv._ATTENTION_WORKSPACES.values(), *nv.kv._COUNTERS.values())]
+        assert None not in own and own[0] != own[1] and not set(own) & set(shared), field
+    for launch, out in launches:
+        out.zero_()
+        for _ in range(3):
+            launch()
+        assert torch.equal(out, want)
+
+
+def test_prepared_gradients_have_buffers_of_their_own():
+    x = torch.randn(50, 4, 64, device="cuda").bfloat16()
+    w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    want = nv.qk_norm_rope_bwd(x, x, x, x, q_weight=w, k_weight=w)
+    launches = [nv.prepare(nv.qk_norm_rope_bwd, x, x, x, x, q_weight=w, k_weight=w) for _ in range(2)]
+    own = [l._args[-1] for l, _ in launches]
+    assert own[0] != own[1] and not set(own) & {t.data_ptr() for t in nv.kv._BWD_WORKSPACES.values()}
+    for launch, got in launches:
+        for _ in range(3):
+            launch()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
