@@ -698,7 +698,9 @@ int nvfp4_kv_read(const nvfp4_kv_cache* cache, const int64_t* slots, int64_t tok
  *             requests are still computed in full).
  *   workspace nvfp4_kv_attention_workspace_bytes(args) bytes, 16-byte
  *             aligned, with any contents; may be NULL where that size is 0.
- *             Overlapping calls need their own.  The bytes depend on tokens,
+ *             Overlapping calls need their own, and calls that several
+ *             threads issue to one stream overlap: a call may be two launches,
+ *             and another one's may come between.  The bytes depend on tokens,
  *             batch, max_seq_len, heads, D, window and whether cu_q is given.
  *   counters  optional NVFP4_KV_COUNTER_BYTES, 16-byte aligned, zero-filled
  *             once (every completed call leaves them zero); overlapping calls

@@ -10,6 +10,7 @@ dense, their tokens may be any multiple of 4 values apart (8 for
 ``kv_attention``).
 """
 import ctypes
+import threading
 from dataclasses import dataclass, field
 from typing import Optional
 
@@ -371,6 +372,10 @@ def kv_read(cache: KVCache, slots: torch.Tensor, *, out: Optional[tuple] = None)
 # ---------------------------------------------------------------- attention
 _ATTENTION_WORKSPACES, _COUNTERS = {}, {}
 KV_COUNTER_BYTES = N.KV_COUNTER_BYTES
+# An attention call may be two launches with one workspace between them, and
+# the library call lets other threads run: none may issue its own in between
+# on the same stream, and so with the same workspace.
+_ISSUE = threading.RLock()
 
 
 def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
@@ -429,9 +434,10 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
         _check(workspace, _U8, "workspace")
         if workspace.numel() < n:
             raise ValueError(f"workspace must hold {n} bytes, got {workspace.numel()}")
-    else:
-        workspace = _cached_workspace(_ATTENTION_WORKSPACES, place, dev, n, 0)
-    args.workspace = _ptr(workspace)
-    _invoke("nvfp4_kv_attention", (ctypes.byref(args),), dev,
-            (q, cache, block_table, seq_lens, cu_q, out, lse, workspace, counters, args))
+    with _ISSUE:
+        if workspace is None:
+            workspace = _cached_workspace(_ATTENTION_WORKSPACES, place, dev, n, 0)
+        args.workspace = _ptr(workspace)
+        _invoke("nvfp4_kv_attention", (ctypes.byref(args),), dev,
+                (q, cache, block_table, seq_lens, cu_q, out, lse, workspace, counters, args))
     return (out, lse) if lse is not None else out

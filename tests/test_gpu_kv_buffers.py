@@ -1,4 +1,6 @@
 """Whose memory the key/value-cache calls use."""
+import threading
+
 import pytest
 
 from helpers import dev_bf16
@@ -49,3 +51,30 @@ def test_prepared_gradients_have_buffers_of_their_own():
             launch()
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+def test_threads_on_one_stream_do_not_mix_their_pieces(monkeypatch):
+    """A call may be two launches with one workspace between them: no other
+    thread's call on that stream may come between."""
+    args = _split_call(42)
+    nv.kv_attention(*args)
+    inside, entered, both = threading.Lock(), [], threading.Event()
+    real = nv.kv._invoke
+
+    def invoke(entry, *rest):
+        with inside:
+            entered.append(threading.get_ident())
+            if len(entered) > 1:
+                both.set()
+        alone = not both.wait(0.5) if entered[0] == threading.get_ident() else True
+        real(entry, *rest)
+        if not alone:
+            entered.append("mixed")
+
+    monkeypatch.setattr(nv.kv, "_invoke", invoke)
+    threads = [threading.Thread(target=nv.kv_attention, args=args) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(entered) == 2 and len(set(entered)) == 2
