@@ -73,12 +73,13 @@ def _heads(x, name, tokens=None, heads=None, dim=None, granule=4):
 
 
 # ---------------------------------------------------------------- cache
-@dataclass
+@dataclass(frozen=True, eq=False)
 class KVCache:
     """The paged NVFP4 cache of one layer: k_codes [P, H, S, D/2], k_scales
     [P, H, S, D/16], v_codes [P, H, S/8, D/2, 8], v_scales [P, H, S/8, D/16, 8]
     (uint8), the calibrated outer amaxes k_amax and v_amax [H] (float32) and
-    S_g.  Slot page * S + i is token i of a page."""
+    S_g.  Slot page * S + i is token i of a page.  The tensors' addresses are
+    taken once: a cache with other ones is another KVCache."""
     k_codes: torch.Tensor
     k_scales: torch.Tensor
     v_codes: torch.Tensor
@@ -104,12 +105,14 @@ class KVCache:
         _need(self.v_scales, torch.uint8, "v_scales", p * h * s * (d // 16))
         _need(self.k_amax, torch.float32, "k_amax", h)
         _need(self.v_amax, torch.float32, "v_amax", h)
-        self.num_pages, self.kv_heads, self.page_size, self.head_dim = p, h, s, d
-        self.global_max = float(self.global_max)
-        self._args = N.KVCacheArgs(
+        sg = float(self.global_max)
+        args = N.KVCacheArgs(
             k_codes=_ptr(self.k_codes), k_scales=_ptr(self.k_scales), v_codes=_ptr(self.v_codes),
             v_scales=_ptr(self.v_scales), k_amax=_ptr(self.k_amax), v_amax=_ptr(self.v_amax),
-            num_pages=p, kv_heads=h, page_size=s, head_dim=d, global_fp8_max=self.global_max)
+            num_pages=p, kv_heads=h, page_size=s, head_dim=d, global_fp8_max=sg)
+        for name, value in (("num_pages", p), ("kv_heads", h), ("page_size", s), ("head_dim", d),
+                            ("global_max", sg), ("_args", args)):
+            object.__setattr__(self, name, value)
 
     @property
     def device(self):

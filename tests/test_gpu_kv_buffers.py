@@ -78,3 +78,13 @@ def test_threads_on_one_stream_do_not_mix_their_pieces(monkeypatch):
     for t in threads:
         t.join()
     assert len(entered) == 2 and len(set(entered)) == 2
+
+
+def test_a_cache_cannot_be_given_other_memory():
+    """The calls pass the addresses that the cache was made with."""
+    cache = _split_call(43)[1]
+    for field, value in (("k_codes", cache.k_codes.clone()), ("v_amax", cache.v_amax.clone()),
+                         ("global_max", 448.0), ("num_pages", 1)):
+        with pytest.raises(AttributeError):
+            setattr(cache, field, value)
+    assert cache == cache and cache != _split_call(43)[1]
