@@ -543,9 +543,11 @@ typedef struct nvfp4_kv_cache {
  * tokens >= the sum of new_lens, or the rest is not planned.  Pages are given
  * back by writing their numbers to free_pages above the count.
  * One launch.  Every pointer is a device pointer with natural alignment.
- * Errors (NVFP4_ERR_INVALID): NULL pointers, batch, tokens or table_width
- * < 0 or > 2^31 - 1, page_size not a power of two in 8 .. 1024, num_pages < 1
- * or > 2^31 - 1.
+ * An output may share no memory with an input or the table (a plan that
+ * goes on from the last one's seq_lens and free_count has two sets).
+ * Errors (NVFP4_ERR_INVALID): NULL pointers, an output that is an input,
+ * batch, tokens or table_width < 0 or > 2^31 - 1, page_size not a power of two
+ * in 8 .. 1024, num_pages < 1 or > 2^31 - 1.
  */
 typedef struct nvfp4_kv_plan_args {
   const int32_t *ctx_lens, *new_lens; /* [batch] */

@@ -87,6 +87,12 @@ int nvfp4_kv_plan(const nvfp4_kv_plan_args* p, hipStream_t stream) {
   if (!given(a.free_pages, 4) || !given(a.free_count, 4) || !given(a.cu_new, 4) ||
       !given(a.free_count_out, 4) || !given(a.refused, 4))
     return NVFP4_ERR_INVALID;
+  // one workgroup writes while another one still reads the inputs
+  const void* const in[] = {a.ctx_lens, a.new_lens, a.free_pages, a.free_count, a.block_table};
+  const void* const out[] = {a.cu_new, a.seq_lens, a.positions, a.slots, a.free_count_out, a.refused};
+  for (const void* o : out)
+    for (const void* i : in)
+      if (o && o == i) return NVFP4_ERR_INVALID;
   return status_of(launch_kv_plan(a, stream));
 }
 

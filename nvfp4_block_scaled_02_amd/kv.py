@@ -144,6 +144,12 @@ class KVPlan:
     refused: torch.Tensor
 
 
+def _span(t):
+    """Addresses [first, last) of a contiguous tensor."""
+    at = t.data_ptr()
+    return at, at + t.numel() * t.element_size()
+
+
 def kv_plan(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
             free_pages: torch.Tensor, free_count: torch.Tensor, *, page_size: int, num_pages: int,
             tokens: int, out: Optional[KVPlan] = None) -> KVPlan:
@@ -151,7 +157,8 @@ def kv_plan(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.T
     requests' lengths; the new pages are written into block_table [batch,
     width] (int32).  free_pages [num_pages] and free_count [1] (int32) are the
     stack of free pages; the result's free_count is the count after the step.
-    tokens: at least the sum of new_lens (the rest is padding)."""
+    tokens: at least the sum of new_lens (the rest is padding).  out: a KVPlan
+    to write, which shares no memory with the inputs."""
     _check(ctx_lens, _I32, "ctx_lens")
     batch = ctx_lens.numel()
     _check(new_lens, _I32, "new_lens", batch)
@@ -173,6 +180,15 @@ def kv_plan(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.T
         _check(out.slots, _I64, "slots", tokens)
         _check(out.free_count, _I32, "free_count", 1)
         _check(out.refused, _I32, "refused", 1)
+        inputs = dict(ctx_lens=ctx_lens, new_lens=new_lens, block_table=block_table,
+                      free_pages=free_pages, free_count=free_count)
+        for name in ("cu_new", "seq_lens", "positions", "slots", "free_count", "refused"):
+            a, b = _span(getattr(out, name))
+            for of, t in inputs.items():
+                c, d = _span(t)
+                if a < d and c < b:
+                    raise ValueError(f"out.{name} and {of} share memory: the call reads its "
+                                     "inputs while it writes its outputs")
     args = N.KVPlanArgs(
         ctx_lens.data_ptr(), new_lens.data_ptr(), batch, block_table.data_ptr(),
         block_table.shape[1], free_pages.data_ptr(), free_count.data_ptr(), num_pages, page_size,

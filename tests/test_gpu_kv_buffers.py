@@ -88,3 +88,24 @@ def test_a_cache_cannot_be_given_other_memory():
         with pytest.raises(AttributeError):
             setattr(cache, field, value)
     assert cache == cache and cache != _split_call(43)[1]
+
+
+def test_plan_outputs_may_not_be_its_inputs():
+    z = lambda n, t=torch.int32: torch.zeros(n, dtype=t, device="cuda")  # noqa: E731
+    ctx, new, table = z(2), z(2) + 1, z(8).view(2, 4)
+    free, count = torch.arange(4, dtype=torch.int32, device="cuda"), z(1) + 4
+    kw = dict(page_size=8, num_pages=4, tokens=2)
+
+    def out(**other):
+        return nv.KVPlan(**{**dict(cu_new=z(3), seq_lens=z(2), positions=z(2), slots=z(2, torch.int64),
+                                   free_count=z(1), refused=z(1)), **other})
+
+    lens = torch.cat([ctx, new])
+    for o, c in ((out(seq_lens=ctx), ctx), (out(seq_lens=new), ctx), (out(free_count=count), ctx),
+                 (out(refused=free[3:]), ctx), (out(positions=table.view(-1)[3:5]), ctx),
+                 (out(seq_lens=lens[1:3]), lens[:2]), (out(slots=lens.view(torch.int64)), lens[:2])):
+        with pytest.raises(ValueError, match="share memory"):
+            nv.kv_plan(c, new, table, free, count, **kw, out=o)
+    # beside each other in one allocation
+    o = out(seq_lens=lens[2:])
+    assert nv.kv_plan(lens[:2], new, table, free, count, **kw, out=o).seq_lens.tolist() == [1, 1]
