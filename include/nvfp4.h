@@ -525,10 +525,10 @@ typedef struct nvfp4_kv_cache {
  * tokens in the cache, in the pages block_table[b, 0 .. ceil(ctx/page_size)),
  * and brings new_lens[b] tokens (negative lengths count as 0); the step's
  * tokens are the requests' new ones, request after request.
- *   - A request whose ctx + new tokens need more than table_width pages is
- *     refused.  The others take pages in order from the top of the stack
- *     free_pages[0 .. *free_count): the i-th page taken is
- *     free_pages[*free_count - 1 - i].  Once the running total of pages
+ *   - A request whose ctx + new tokens need more than table_width pages, or
+ *     are more than 2^31 - 1, is refused.  The others take pages in order from
+ *     the top of the stack free_pages[0 .. *free_count): the i-th page taken
+ *     is free_pages[*free_count - 1 - i].  Once the running total of pages
  *     needed passes *free_count, every request that needs a page is refused.
  *     A refused request takes none; *refused counts them.
  *   - block_table receives the new pages of the admitted requests; nothing

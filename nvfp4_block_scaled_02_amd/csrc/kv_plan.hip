@@ -77,7 +77,8 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(nvfp4_kv_plan_arg
     }
     const int64_t have = (ctx + page_size - 1) >> shift;
     const int64_t need = (ctx + fresh + page_size - 1) >> shift;
-    const bool fits = need <= a.table_width;
+    // lengths and positions are 32-bit numbers, whatever the table has room for
+    const bool fits = need <= a.table_width && ctx + fresh <= INT32_MAX;
     const int64_t more = fits ? need - have : 0;
     Pair64 total;
     const Pair64 sum = block_scan(Pair64{fresh, more}, wave_sums, total);
