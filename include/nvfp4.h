@@ -526,10 +526,11 @@ typedef struct nvfp4_kv_cache {
  * and brings new_lens[b] tokens (negative lengths count as 0); the step's
  * tokens are the requests' new ones, request after request.
  *   - A request whose ctx + new tokens need more than table_width pages, or
- *     are more than 2^31 - 1, is refused.  The others take pages in order from
- *     the top of the stack free_pages[0 .. *free_count): the i-th page taken
- *     is free_pages[*free_count - 1 - i].  Once the running total of pages
- *     needed passes *free_count, every request that needs a page is refused.
+ *     are more than 2^31 - 1, or whose new tokens do not all lie in [0,
+ *     tokens), is refused.  The others take pages in order from the top of the
+ *     stack free_pages[0 .. *free_count): the i-th page taken is
+ *     free_pages[*free_count - 1 - i].  Once the running total of pages needed
+ *     passes *free_count, every request that needs a page is refused.
  *     A refused request takes none; *refused counts them.
  *   - block_table receives the new pages of the admitted requests; nothing
  *     else of it changes.
@@ -540,8 +541,7 @@ typedef struct nvfp4_kv_cache {
  *     page of this cache.  Tokens from cu_new[batch] on (padding): 0 and -1.
  *   - *free_count_out = *free_count - pages taken (the inputs stay, so the
  *     call can be repeated).
- * tokens >= the sum of new_lens, or the rest is not planned.  Pages are given
- * back by writing their numbers to free_pages above the count.
+ * Pages are given back by writing their numbers to free_pages above the count.
  * One launch.  Every pointer is a device pointer with natural alignment.
  * An output may share no memory with an input or the table (a plan that
  * goes on from the last one's seq_lens and free_count has two sets).

@@ -82,7 +82,10 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(nvfp4_kv_plan_arg
     const int64_t more = fits ? need - have : 0;
     Pair64 total;
     const Pair64 sum = block_scan(Pair64{fresh, more}, wave_sums, total);
-    const bool ok = fits && (more == 0 || page0 + sum.b <= free_count);
+    // new tokens that the step has no room for: their ends ascend, so no
+    // request behind such a one is admitted to a page either
+    const bool room = fresh == 0 || tok0 + sum.a <= a.tokens;
+    const bool ok = fits && room && (more == 0 || page0 + sum.b <= free_count);
     req[threadIdx.x] = Request{tok0 + sum.a - fresh, page0 + sum.b - more, (int32_t)ctx, (int32_t)have, ok, 0};
     if (blockIdx.x == 0 && b < a.batch) {
       a.cu_new[b + 1] = (int32_t)(tok0 + sum.a);
@@ -90,20 +93,19 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(nvfp4_kv_plan_arg
       if (!ok) atomicAdd(&refused_here, 1);
     }
     // pages taken: the running total of the last admitted request (totals
-    // ascend, so those within the free count are a prefix)
+    // ascend, so those within the free count and the tokens are a prefix)
     __syncthreads();
     if (blockIdx.x == 0 && threadIdx.x == 0) {
-      // nothing is taken past the first running total that exceeds the count
-      if (page0 + total.b <= free_count) taken = page0 + total.b;
-      else if (page0 <= free_count) {
-        int lo = 0, hi = kPlanThreads;  // first request whose total exceeds it
+      const auto within = [&](int64_t tokens, int64_t pages) { return tokens <= a.tokens && pages <= free_count; };
+      if (within(tok0 + total.a, page0 + total.b)) taken = page0 + total.b;
+      else if (within(tok0, page0)) {
+        int lo = 0, hi = kPlanThreads - 1;  // first request past either: at the latest the chunk's last
         while (lo < hi) {
           const int mid = (lo + hi) >> 1;
-          const int64_t upto = mid + 1 < kPlanThreads ? req[mid + 1].page0 : page0 + total.b;
-          if (upto <= free_count) lo = mid + 1;
+          if (within(req[mid + 1].first, req[mid + 1].page0)) lo = mid + 1;
           else hi = mid;
         }
-        taken = lo < kPlanThreads ? req[lo].page0 : page0 + total.b;
+        taken = req[lo].page0;
       }
     }
     const int64_t end = tok0 + total.a;

@@ -157,8 +157,9 @@ def kv_plan(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.T
     requests' lengths; the new pages are written into block_table [batch,
     width] (int32).  free_pages [num_pages] and free_count [1] (int32) are the
     stack of free pages; the result's free_count is the count after the step.
-    tokens: at least the sum of new_lens (the rest is padding).  out: a KVPlan
-    to write, which shares no memory with the inputs."""
+    tokens: at least the sum of new_lens (the rest is padding; a request that
+    does not fit into it is refused).  out: a KVPlan to write, which shares
+    no memory with the inputs."""
     _check(ctx_lens, _I32, "ctx_lens")
     batch = ctx_lens.numel()
     _check(new_lens, _I32, "new_lens", batch)
