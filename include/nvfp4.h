@@ -534,8 +534,8 @@ typedef struct nvfp4_kv_cache {
  *     A refused request takes none; *refused counts them.
  *   - block_table receives the new pages of the admitted requests; nothing
  *     else of it changes.
- *   - cu_new [batch + 1] = running total of new tokens; seq_lens [batch] =
- *     ctx + new, or ctx where refused.
+ *   - cu_new [batch + 1] = running total of new tokens (at most 2^31 - 1);
+ *     seq_lens [batch] = ctx + new, or ctx where refused.
  *   - positions [tokens]: the token's place in its request; slots [tokens]:
  *     its slot, -1 for a refused request's token or where the table holds no
  *     page of this cache.  Tokens from cu_new[batch] on (padding): 0 and -1.

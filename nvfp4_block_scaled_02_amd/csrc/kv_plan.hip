@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(nvfp4_kv_plan_arg
     const bool ok = fits && room && (more == 0 || page0 + sum.b <= free_count);
     req[threadIdx.x] = Request{tok0 + sum.a - fresh, page0 + sum.b - more, (int32_t)ctx, (int32_t)have, ok, 0};
     if (blockIdx.x == 0 && b < a.batch) {
-      a.cu_new[b + 1] = (int32_t)(tok0 + sum.a);
+      a.cu_new[b + 1] = (int32_t)(tok0 + sum.a < INT32_MAX ? tok0 + sum.a : INT32_MAX);
       a.seq_lens[b] = (int32_t)(ok ? ctx + fresh : ctx);
       if (!ok) atomicAdd(&refused_here, 1);
     }

@@ -43,3 +43,12 @@ def test_requests_past_the_steps_tokens_are_refused():
         slots = p.slots.tolist()
         assert all(s >= 0 for s in slots[:5]) and all((s >= 0) == (lens[1] == 56) for s in slots[5:45])
         assert all((s >= 0) == (lens[2] == 3) for s in slots[45:48])
+
+
+def test_running_totals_stay_in_32_bits():
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    top = 2**31 - 1
+    p = nv.kv_plan(i32([0, 0, 0, 4]), i32([3, top, top, 0]), torch.zeros(4, 2, dtype=torch.int32, device="cuda"),
+                   i32([1, 2]), i32([2]), page_size=16, num_pages=2, tokens=3)
+    assert p.cu_new.tolist() == [0, 3, top, top, top] and p.seq_lens.tolist() == [3, 0, 0, 4]
+    assert int(p.refused) == 2 and int(p.free_count) == 1
