@@ -616,10 +616,11 @@ int nvfp4_qk_norm_rope(const nvfp4_qk_args* args, hipStream_t stream);
  * rotated back, n = x * r and r = (mean(x^2) + eps)^-1/2:
  *   dx = r * (g w - n * mean(g w n)),  dw = sum over tokens and heads of g n
  * (w NULL: dx = g, no dw), in binary32 (r of heads whose squares leave it in
- * binary64), dw's sums in binary64 in a fixed order.  At eps = 0 a head of zeros is 0 / 0: NaN in its dx and in dw.
- * args->q, k and the tables as in the forward call; args->q_out and
- * k_out with their strides are the OUTPUTS dq and dk (bf16); dq_out, dk_out
- * the incoming gradients (bf16) with strides gq_stride and gk_stride.
+ * binary64), dw's sums in binary64 in a fixed order.  At eps = 0 a head of
+ * zeros is 0 / 0: NaN in its dx and in dw.  args->q, k and the tables as in
+ * the forward call; args->q_out and k_out with their strides are the OUTPUTS
+ * dq and dk (bf16); dq_out, dk_out the incoming gradients (bf16) with strides
+ * gq_stride and gk_stride.
  *   dq_weight, dk_weight  float [D], required exactly where the weight is.
  *   workspace   nvfp4_qk_norm_rope_bwd_workspace_bytes(head_dim) bytes of
  *               device memory, 16-byte aligned, zero-filled once before its
@@ -644,7 +645,8 @@ int nvfp4_qk_norm_rope_bwd(const nvfp4_qk_args* args, const uint16_t* dq_out, in
  * head as A and the cache's global_fp8_max as S_g) with args->select =
  * NVFP4_SELECT_6 or NVFP4_SELECT_4OVER6.  Token t goes to slots[t]; a slot
  * outside [0, num_pages * page_size) writes nothing (its query is still
- * returned).  Slots of one call are distinct, or either token may be kept.
+ * returned).  Slots of one call are distinct, or such a slot holds a mix of
+ * its tokens.
  * Errors: as nvfp4_qk_norm_rope (qk.k, k_heads = cache.kv_heads and head_dim
  * = cache.head_dim required) and the cache's rules; NULL or misaligned v or
  * slots; another select -> NVFP4_ERR_INVALID (known rules:
@@ -688,7 +690,7 @@ int nvfp4_kv_read(const nvfp4_kv_cache* cache, const int64_t* slots, int64_t tok
  * power of two per row and held in binary16 (exact for values within 2^-14 of
  * the row's largest, and nearer than 2^-25 of it below); scores, maxima, sums
  * and outputs accumulate in binary32 (scores past 10^8 in magnitude, which it
- * no longer tells apart, may give NaN).  The softmax weights round once to
+ * no longer tells apart, may give NaN or 0).  The softmax weights round once to
  * binary16, in the output's sums and in lse alike: each by 2^-11 of itself or
  * by 2^-32 of the row's largest, whichever is more, so that n keys far below
  * one large score may lose up to n 2^-32 of the row's sum.

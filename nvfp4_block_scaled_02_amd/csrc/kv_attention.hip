@@ -32,11 +32,13 @@
 // keys once, into LDS.
 //
 // Measured with 32 query and 8 key heads of 128 values: 64 requests of 8191
-// keys 115 us (5.3 TB/s, the rate of a copy), of up to 8192 78 .. 84 (341 MB,
-// 66 us at that rate; vector units 59 % busy, matrix units 16), one of 8191
-// keys 10.7; 2 x 2048 tokens behind 6000 cached ones 355 .. 361 us, 880 to 900
-// TFLOP/s (263 us at the rate of a large product; vector units 55 % busy with
-// softmax and dequantization, matrix units 41), a prompt of 8191 tokens 582.
+// keys 112 .. 115 us (5.3 TB/s, the rate of a copy), of up to 8192 78 .. 84
+// (341 MB, 66 us at that rate; vector units 59 % busy, matrix units 16), one of
+// 8191 keys 10.5; 2 x 2048 tokens behind 6000 cached ones 353 .. 362 us, 880 to
+// 900 TFLOP/s (263 us at the rate of a large product; vector units 54 % busy
+// with softmax and dequantization, matrix units 41: a wavefront runs scores,
+// softmax and products one after the other, and a SIMD has two of them to
+// overlap), a prompt of 8191 tokens 572 .. 582.
 #include <math.h>
 
 #include "kv.hpp"
@@ -1107,7 +1109,13 @@ kv_attention_rows_kernel(AttnArgs args) {
 AttnPlan kv_attention_plan(const nvfp4_kv_attention_args& a) {
   AttnPlan p = {};
   const int D = a.cache.head_dim, group = a.q_heads / a.cache.kv_heads;
-  // rows of an average request decide the form; every form is right for all
+  // Rows of an average request decide the form; every form is right for all.
+  // Many rows: 2 x 2048 tokens behind 6000 cached ones 392 us against 801 in
+  // the other form.  That form never cuts the keys, though, so few tiles over a
+  // long axis cost what one workgroup takes to walk it: 31 tokens (124 rows)
+  // behind 32768 keys of 8 heads 46 us, 32 tokens 863 and 256 tokens 878.  And
+  // one form serves a whole call: 64 single tokens over 4096 keys beside a
+  // chunk of 2048 take 246 us, one after the other 56 and 134.
   const int64_t batch = a.batch > 0 ? a.batch : 1;
   const int64_t rows = a.cu_q ? (a.tokens * group + batch - 1) / batch : group;
   const int nq_most = keys_nq_most(D);

@@ -75,9 +75,11 @@ __device__ __forceinline__ void quad_quantize(const float (&x)[8], const TensorS
 // Heads of a token: queries (normed, rotated, returned), keys (normed,
 // rotated, quantized), values (quantized).  A value's bytes lie eight tokens
 // apart, so its stores are single bytes that meet in the L2.  Bound by the
-// vector units (81 % busy; max->6 and max->4 are both encoded and compared):
-// 8192 tokens of 32 + 8 + 8 heads of 128 move 187 MB in 44 us, the keys' and
-// values' part alone 25; 64 single tokens 4.9 us.
+// vector units (81 % busy with 4/6, where max->6 and max->4 are both encoded
+// and compared, 74 with max->6) and by bytes: 8192 tokens of 32 + 8 + 8 heads of
+// 128 move 187 MB in 44 us, in a loop of launches in 42.4 and, with max->6,
+// 41.1; the keys' and values' part alone takes 23.0 and 20.0.  64 single tokens
+// 5.0 us.
 template <int LPH, int PAIRS, int SELECT>
 __global__ void __launch_bounds__(kRowThreads)
 kv_append_kernel(nvfp4_kv_append_args p, RowGrid grid) {
@@ -183,7 +185,7 @@ hipError_t launch_kv_append(const nvfp4_kv_append_args& a, hipStream_t s) {
 
 // ---------------------------------------------------------------- read
 // 8192 tokens of 8 heads of 128 keys and values (51 MB, 34 of them written):
-// 12.3 us; 64 tokens 3.8 us.
+// 12.4 us; 64 tokens 3.6 us.
 template <int LPH>
 __global__ void __launch_bounds__(kRowThreads)
 kv_read_kernel(nvfp4_kv_cache c, const int64_t* slots, RowGrid grid, uint16_t* k_out, uint16_t* v_out) {

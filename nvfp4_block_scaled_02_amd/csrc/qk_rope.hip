@@ -158,9 +158,10 @@ __device__ __forceinline__ double sum_slots(const double* slots, int n, int e, i
 // 32 teams adds the team's slots in order, the last team the teams' sums: no
 // atomic addition, the same bits on every run.  Slots are written and read at
 // the level that the whole GPU sees, so no cache is written back.
-// Bound by its bytes: 261 MB (254 without the partial sums) in 50 us at 8192
-// tokens of 32 + 8 heads of 128, 5.2 TB/s with the vector units 71 % busy;
-// 1023 tokens of 12 + 4 heads of 64 take 12.3 us, most of it latency.
+// Bound by its bytes: 261 MB (254 without the partial sums) in 51 us at 8192
+// tokens of 32 + 8 heads of 128, 5.1 TB/s with the vector units 75 % busy;
+// 1023 tokens of 12 + 4 heads of 64 take 12.6 us, most of it latency: of the
+// loads, and of the two levels that join up to 1024 workgroups' sums.
 template <int LPH, int PAIRS>
 __global__ void __launch_bounds__(kRowThreads, 4)
 qk_norm_rope_bwd_kernel(BwdArgs b) {

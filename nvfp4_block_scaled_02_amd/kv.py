@@ -412,7 +412,7 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
     width); scale: default D^-1/2; window: attend the last `window` tokens only
     (0: all).  Returns out [tokens, q_heads, D] bf16, or (out, lse) with
     want_lse.  workspace: a uint8 tensor of at least the size the library asks
-    for.  counters: a uint8 tensor of KV_COUNTER_BYTES zeros, which every call
+    for (a stream's own grows to the largest asked for and is kept).  counters: a uint8 tensor of KV_COUNTER_BYTES zeros, which every call
     leaves zero; with it few pieces of a split sequence are joined in the same
     launch.  Without them a call uses its stream's (a prepared Launch its own,
     for runs that do not overlap), and under graph capture a new workspace and
